@@ -1,0 +1,392 @@
+// int8.cuh -- the matrix product in 8-bit integers with one scale a token and
+// one a channel, on tcgen05 (kind::i8, int32 accumulation in TMEM):
+//
+//   out[r, n] = bf16( sum_k xq[r, k] Wq[e, n, k]  *  sx[r]  *  sw[e, n] )
+//
+// of one weight matrix for every row (dense, e = 0) or of expert e's matrix for
+// the rows offsets[e] .. offsets[e + 1) (grouped).  The sum is exact: a product
+// is at most 2^14, so K <= 2^16 keeps it below 2^30; it is rounded to fp32 once,
+// scaled in fp32 and rounded to bf16 once.
+//
+// As in the bf16 expert GEMM the weights fill the M slot (128 channels) and the
+// rows the N slot (16..256), so a decode batch costs a 16-wide MMA.  A K block is
+// 128 codes, one 128-byte swizzle row; the last one of a K that is not a
+// multiple of 128 is filled with zeros by the TMA.  Three forms:
+//
+//   I8_SINGLE  one CTA a tile, persistent over the tile list
+//   I8_PAIR    CTA pairs (cta_group::2): 256 channels a tile, each CTA loads its
+//              128 channels and half of the rows -- two thirds of the shared
+//              memory traffic per MMA, which bounds wide tiles of 8-bit operands
+//   I8_SPLIT   a cluster of 2, 4 or 8 CTAs shares one tile's K range and adds
+//              the int32 sums through distributed shared memory: dense products
+//              with fewer tiles than SMs, bound by the weights' bytes.  The sums
+//              are integers, so the split changes no bit.
+//
+// Warp roles as in grouped_gemm.cuh: warp 0 TMA producer, warp 1 MMA issuer,
+// warps 2-5 epilogue; two TMEM accumulators of 256 columns; every wait is
+// bounded.  All loads come after griddepcontrol.wait: weights may be the output
+// of the kernel before (a quantiser).
+#pragma once
+
+#include "common.cuh"
+#include "grouped_gemm.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+
+constexpr int I8_SINGLE = 0, I8_PAIR = 1, I8_SPLIT = 2;
+constexpr int kI8BlockK = 128;                   // codes per K block
+constexpr int kI8MaxK = 1 << 16;
+constexpr int kI8RingBytes = 200 * 1024;
+constexpr int kI8SmemBytes = 1024 + kI8RingBytes + kBarBytes + (int)sizeof(SmemPlan);
+static_assert(kI8SmemBytes <= 227 * 1024, "shared memory budget");
+static_assert(128 * 256 * 4 <= kI8RingBytes, "the int32 tile of I8_SPLIT reuses the ring");
+
+struct Int8Args {
+    const int32_t* plan;    // grouped: the tile plan; dense: null
+    int T;                  // rows; dense: cut into `units` chunks of `chunk` rows
+    int units, chunk;
+    int N, K;
+    const float* sx;        // [rows]
+    const float* sw;        // [E, N]
+    bf16* out;              // [rows, N]
+    uint32_t* err;
+};
+
+struct I8Tile {
+    int e, m, row0, rows, n_mma, ma, b_row0, b_n;
+};
+
+// Tile t of the launch.  rank: this CTA's place in its pair.
+template <int FORM>
+__device__ __forceinline__ I8Tile i8_tile(int t, int nb, const Int8Args& a, const SmemPlan* sp, int rank)
+{
+    constexpr int kRows = FORM == I8_PAIR ? 256 : 128;
+    I8Tile tl;
+    int start, row_base, n;
+    const int mt = (a.N + kRows - 1) / kRows;
+    if (!a.plan) {
+        const int u = t / mt;
+        tl.m = t - u * mt;
+        tl.e = 0;
+        start = u * a.chunk;
+        row_base = 0;
+        n = min(a.chunk, a.T - start);
+    } else {
+        int lo = 0, hi = nb - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (sp->tb[mid] <= t) lo = mid;
+            else hi = mid - 1;
+        }
+        const int local = t - sp->tb[lo], units = sp->units[lo];
+        const int4 b = sp->blk[lo];
+        tl.e = b.x;
+        tl.m = local / units;
+        start = (local - tl.m * units) * b.w;
+        row_base = b.y;
+        n = min(b.w, b.z - start);
+    }
+    tl.rows = n;
+    tl.row0 = row_base + start;
+    tl.n_mma = FORM == I8_PAIR ? (n + 31) & ~31 : (n + 15) & ~15;
+    if (FORM == I8_PAIR) {
+        tl.ma = 2 * tl.m + rank;
+        tl.b_n = tl.n_mma >> 1;
+        tl.b_row0 = tl.row0 + rank * tl.b_n;
+    } else {
+        tl.ma = tl.m;
+        tl.b_n = tl.n_mma;
+        tl.b_row0 = tl.row0;
+    }
+    return tl;
+}
+
+template <int FORM>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    int8_gemm_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB16,
+                     const __grid_constant__ CUtensorMap mB64, const Int8Args a)
+{
+    constexpr bool PAIR = FORM == I8_PAIR;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    SmemCtl* ctl = reinterpret_cast<SmemCtl*>(smem + kI8RingBytes);
+    SmemPlan* splan = reinterpret_cast<SmemPlan*>(smem + kI8RingBytes + kBarBytes);
+    const uint32_t ring = ptx::smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = FORM != I8_SINGLE ? (int)ptx::cluster_ctarank() : 0;
+    const bool leader = !PAIR || rank == 0;
+    const int split = FORM == I8_SPLIT ? (int)(gridDim.x / ptx::nclusters_x()) : 1;   // CTAs that share a tile
+    const int first = FORM == I8_SINGLE ? (int)blockIdx.x : (int)ptx::cluster_id_x();
+    const int step = FORM == I8_SINGLE ? (int)gridDim.x : (int)ptx::nclusters_x();
+
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const PlanHeader* hdr = reinterpret_cast<const PlanHeader*>(a.plan);
+    const int nb = a.plan ? hdr->n_blocks : 0;
+    constexpr int kRows = PAIR ? 256 : 128;
+    const int total = a.plan ? hdr->tiles2 : a.units * ((a.N + kRows - 1) / kRows);
+    const int widest = a.plan ? hdr->n_max : min(a.chunk, a.T);
+    const int n_max = PAIR ? max(32, (widest + 31) & ~31) : max(16, (widest + 15) & ~15);
+    const uint32_t stage_bytes = kATileBytes + (uint32_t)(PAIR ? n_max / 2 : n_max) * kBRowBytes;
+    const int stages = min(kMaxStages, (int)(kI8RingBytes / stage_bytes));
+    const int nk = (a.K + kI8BlockK - 1) / kI8BlockK;
+    // I8_SPLIT: this CTA's K blocks (the host launches no more CTAs a tile than K blocks)
+    const int kb0 = FORM == I8_SPLIT ? (int)((int64_t)nk * rank / split) : 0;
+    const int kb1 = FORM == I8_SPLIT ? (int)((int64_t)nk * (rank + 1) / split) : nk;
+
+    if (a.plan) {
+        const PlanArrays pa = plan_arrays(const_cast<int32_t*>(a.plan));
+        // counts and offsets are the caller's: segments outside the rows, or a plan cut
+        // for the other form, are refused by every CTA alike before any barrier
+        bool bad = hdr->pair != (PAIR ? 1 : 0);
+        for (int i = threadIdx.x; i <= nb; i += blockDim.x) {
+            splan->tb[i] = pa.tb2[i];
+            if (i < nb) {
+                const int4 b = make_int4(pa.group[i], pa.row0[i], pa.rows[i], pa.chunk[i]);
+                bad |= b.y < 0 || b.z <= 0 || b.z > a.T || b.y > a.T - b.z;
+                splan->blk[i] = b;
+                splan->units[i] = pa.units[i];
+            }
+        }
+        if (__syncthreads_or(bad)) {
+            if (threadIdx.x == 0) atomicOr(a.err, DEVERR_PLAN);
+            return;
+        }
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; s++) {
+            ptx::mbar_init(ptx::smem_u32(&ctl->full[s]), 1);
+            ptx::mbar_init(ptx::smem_u32(&ctl->empty[s]), 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            ptx::mbar_init(ptx::smem_u32(&ctl->tfull[i]), 1);
+            ptx::mbar_init(ptx::smem_u32(&ctl->tempty[i]), PAIR ? 8 : 4);
+        }
+        ptx::mbar_init(ptx::smem_u32(&ctl->drain), 1);
+        ctl->abort = 0;
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (warp == 0 && lane == 0) {
+        ptx::prefetch_tensormap(&mA);
+        ptx::prefetch_tensormap(&mB16);
+        ptx::prefetch_tensormap(&mB64);
+    }
+    if (warp == 1) {
+        if (PAIR) {
+            ptx::tmem_alloc_pair(ptx::smem_u32(&ctl->tmem_base), kTmemCols);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(ptx::smem_u32(&ctl->tmem_base), kTmemCols);
+            ptx::tmem_relinquish();
+        }
+    }
+    ptx::tc_fence_before();
+    if (PAIR) ptx::cluster_sync();
+    else __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = ctl->tmem_base;
+    auto leader_bar = [&](uint64_t* bar) -> uint32_t {
+        return PAIR ? ptx::mapa_shared(ptx::smem_u32(bar), 0) : ptx::smem_u32(bar);
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        if (ptx::elect_one()) {
+            const uint64_t pol = ptx::policy_evict_normal();
+            uint32_t armed = 0, armed_ph = 0;
+            bool ok = true;
+            int s = 0;
+            uint32_t ph = 0;
+            for (int t = first; ok && t < total; t += step) {
+                const I8Tile tl = i8_tile<FORM>(t, nb, a, splan, rank);
+                const int a_row = tl.e * a.N + tl.ma * 128;
+                const uint32_t tx = (PAIR ? 2u : 1u) * (kATileBytes + (uint32_t)tl.b_n * kBRowBytes);
+                for (int kb = kb0; kb < kb1; kb++) {
+                    if (!bounded_wait(ptx::smem_u32(&ctl->empty[s]), ph ^ 1u, ctl, a.err)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t a_dst = ring + (uint32_t)s * stage_bytes;
+                    const uint32_t full = leader_bar(&ctl->full[s]);
+                    if (leader) {
+                        ptx::mbar_arrive_expect_tx(ptx::smem_u32(&ctl->full[s]), tx);
+                        armed |= 1u << s;
+                        armed_ph = (armed_ph & ~(1u << s)) | (ph << s);
+                    }
+                    const int kc = kb * kI8BlockK;
+                    tma_load<PAIR>(a_dst, &mA, full, kc, a_row, pol);
+                    const uint32_t b_dst = a_dst + kATileBytes;
+                    const int n64 = tl.b_n >> 6;
+                    for (int i = 0; i < n64; i++)
+                        tma_load<PAIR>(b_dst + i * 64 * kBRowBytes, &mB64, full, kc, tl.b_row0 + 64 * i, pol);
+                    for (int r = n64 * 64; r < tl.b_n; r += 16)
+                        tma_load<PAIR>(b_dst + r * kBRowBytes, &mB16, full, kc, tl.b_row0 + r, pol);
+                    if (++s == stages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                // drain (bounded): every stage armed here has landed before the block leaves
+                const uint64_t t0 = ptx::globaltimer();
+                for (int i = 0; i < stages; i++) {
+                    if (!(armed >> i & 1u)) continue;
+                    const uint32_t bar = ptx::smem_u32(&ctl->full[i]);
+                    while (!ptx::mbar_try_wait(bar, (armed_ph >> i) & 1u) &&
+                           ptx::globaltimer() - t0 < kWaitTimeoutNs) {
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (the leader of a pair)
+        if (leader && ptx::elect_one()) {
+            int s = 0, acc = 0;
+            uint32_t ph = 0, aph = 0;
+            bool ok = true, issued = false;
+            for (int t = first; ok && t < total; t += step) {
+                const I8Tile tl = i8_tile<FORM>(t, nb, a, splan, rank);
+                if (!bounded_wait(ptx::smem_u32(&ctl->tempty[acc]), aph ^ 1u, ctl, a.err)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (uint32_t)acc * 256u;
+                const uint32_t idesc = ptx::idesc_s8_s32(PAIR ? 256 : 128, (uint32_t)tl.n_mma);
+                for (int kb = kb0; kb < kb1; kb++) {
+                    if (!bounded_wait(ptx::smem_u32(&ctl->full[s]), ph, ctl, a.err)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t a_addr = ring + (uint32_t)s * stage_bytes;
+                    const uint32_t b_addr = a_addr + kATileBytes;
+#pragma unroll
+                    for (int kk = 0; kk < kI8BlockK / 32; kk++) {
+                        const uint64_t ad = ptx::sw128_kmajor_desc(a_addr + kk * 32);
+                        const uint64_t bd = ptx::sw128_kmajor_desc(b_addr + kk * 32);
+                        const uint32_t accum = (kb > kb0 || kk > 0) ? 1u : 0u;
+                        if (PAIR) ptx::mma_i8_ss_pair(d_tmem, ad, bd, idesc, accum);
+                        else ptx::mma_i8_ss(d_tmem, ad, bd, idesc, accum);
+                    }
+                    issued = true;
+                    if (PAIR) ptx::mma_commit_pair(ptx::smem_u32(&ctl->empty[s]), 3);
+                    else ptx::mma_commit(ptx::smem_u32(&ctl->empty[s]));
+                    if (++s == stages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if (PAIR) ptx::mma_commit_pair(ptx::smem_u32(&ctl->tfull[acc]), 3);
+                else ptx::mma_commit(ptx::smem_u32(&ctl->tfull[acc]));
+                acc ^= 1;
+                if (acc == 0) aph ^= 1u;
+            }
+            if (!ok && issued) {
+                if (PAIR) ptx::mma_commit_pair(ptx::smem_u32(&ctl->drain), 1);
+                else ptx::mma_commit(ptx::smem_u32(&ctl->drain));
+                const uint64_t t0 = ptx::globaltimer();
+                while (!ptx::mbar_try_wait(ptx::smem_u32(&ctl->drain), 0) &&
+                       ptx::globaltimer() - t0 < kWaitTimeoutNs) {
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue (warps 2-5)
+        const int quad = warp & 3;
+        int acc = 0;
+        uint32_t aph = 0;
+        for (int t = first; t < total; t += step) {
+            const I8Tile tl = i8_tile<FORM>(t, nb, a, splan, rank);
+            // scales, fetched before the accumulator wait: a channel a lane, rows l + 32 i of lane l
+            const int ch = tl.ma * 128 + quad * 32 + lane;
+            const float sw = (FORM != I8_SPLIT && ch < a.N) ? __ldg(a.sw + (size_t)tl.e * a.N + ch) : 0.f;
+            float sx[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int col = 32 * i + lane;
+                sx[i] = (FORM != I8_SPLIT && col < tl.rows) ? __ldg(a.sx + tl.row0 + col) : 0.f;
+            }
+            const bool ok = bounded_wait(ptx::smem_u32(&ctl->tfull[acc]), aph, ctl, a.err);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            ptx::tc_fence_after();
+            const uint32_t taddr = tmem_base + (uint32_t)acc * 256u + ((uint32_t)(quad * 32) << 16);
+            for (int c0 = 0; c0 < tl.n_mma; c0 += 16) {
+                uint32_t v[16];
+                ptx::tmem_ld16(taddr + (uint32_t)c0, v);
+                ptx::tmem_ld_wait();
+                if (FORM == I8_SPLIT) {
+                    // this CTA's int32 sums, [column][channel], over the ring: every load of
+                    // it has been consumed and the cluster runs one tile
+                    int* red = reinterpret_cast<int*>(smem);
+#pragma unroll
+                    for (int j = 0; j < 16; j++)
+                        red[(c0 + j) * 128 + quad * 32 + lane] = (int)v[j];
+                } else {
+                    const int gi = c0 >> 5;
+                    const float mine = gi == 0 ? sx[0] : gi == 1 ? sx[1] : gi == 2 ? sx[2] : gi == 3 ? sx[3]
+                                     : gi == 4 ? sx[4] : gi == 5 ? sx[5] : gi == 6 ? sx[6] : sx[7];
+#pragma unroll
+                    for (int j = 0; j < 16; j++) {
+                        const float sc = __shfl_sync(0xffffffffu, mine, (c0 & 31) + j);
+                        const int col = c0 + j;
+                        if (col < tl.rows && ch < a.N)
+                            a.out[(size_t)(tl.row0 + col) * a.N + ch] =
+                                __float2bfloat16_rn((float)(int)v[j] * sc * sw);
+                    }
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR) ptx::mbar_arrive_cluster(leader_bar(&ctl->tempty[acc]));
+                else ptx::mbar_arrive(ptx::smem_u32(&ctl->tempty[acc]));
+            }
+            acc ^= 1;
+            if (acc == 0) aph ^= 1u;
+        }
+    }
+
+    ptx::tc_fence_before();
+    if (FORM != I8_SINGLE) ptx::cluster_sync();
+    else __syncthreads();
+    if (FORM == I8_SPLIT) {
+        // every CTA of the cluster adds a share of the tile: the flattened (column,
+        // 4 channels) items, dealt over the cluster's threads
+        if (first < total) {
+            const I8Tile tl = i8_tile<FORM>(first, nb, a, splan, rank);
+            const int items = tl.rows * 32;
+            for (int i = rank * kGemmThreads + (int)threadIdx.x; i < items; i += split * kGemmThreads) {
+                const int col = i >> 5, c4 = (i & 31) * 4;
+                const int ch = tl.ma * 128 + c4;
+                if (ch >= a.N) continue;       // N % 4 == 0: all four channels or none
+                int sum[4] = {0, 0, 0, 0};
+                for (int p = 0; p < split; p++) {
+                    int v[4];
+                    ptx::ld_cluster_v4(ptx::mapa_shared(ring + (uint32_t)(col * 128 + c4) * 4u, p), v);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) sum[j] += v[j];
+                }
+                const float sx = __ldg(a.sx + tl.row0 + col);
+                const float4 sw = __ldg(reinterpret_cast<const float4*>(a.sw + ch));
+                __nv_bfloat162 lo = __floats2bfloat162_rn((float)sum[0] * sx * sw.x, (float)sum[1] * sx * sw.y);
+                __nv_bfloat162 hi = __floats2bfloat162_rn((float)sum[2] * sx * sw.z, (float)sum[3] * sx * sw.w);
+                *reinterpret_cast<uint2*>(a.out + (size_t)(tl.row0 + col) * a.N + ch) =
+                    make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+            }
+        }
+        ptx::cluster_sync();   // no CTA leaves while another may still read its sums
+    }
+    __syncwarp();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        if (PAIR) ptx::tmem_dealloc_pair(tmem_base, kTmemCols);
+        else ptx::tmem_dealloc(tmem_base, kTmemCols);
+    }
+}
+
+}  // namespace moe

@@ -22,10 +22,13 @@
 #include "common.cuh"
 #include "fp8.cuh"
 #include "grouped_gemm.cuh"
+#include "int8.cuh"
+#include "norm.cuh"
 #include "permute.cuh"
 #include "ptx.cuh"
 #include "route.cuh"
 #include "schedule.h"
+#include "sorted_rows.cuh"
 #include "tile_table.h"
 
 using namespace moe;
@@ -40,6 +43,7 @@ struct DeviceState {
     int sm_count = 0;
     int pair_grid = 0;       // CTAs of a CTA-pair GEMM launch: 2 x the clusters that fit at once (0: none)
     int fp8_pair_grid = 0;   // the same for the FP8 / FP4 GEMM
+    int i8_pair_grid = 0;    // the same for the int8 product
 };
 
 std::mutex g_mu;
@@ -74,10 +78,10 @@ cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-// The same with clusters of two CTAs (the CTA-pair GEMMs).
+// The same with clusters of `ctas` CTAs.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pair(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                        Args&&... args)
+cudaError_t launch_cluster(void (*kernel)(KArgs...), int ctas, dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                           Args&&... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -88,7 +92,7 @@ cudaError_t launch_pair(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t 
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.x = ctas;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -96,6 +100,14 @@ cudaError_t launch_pair(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t 
     g_launches.fetch_add(1, std::memory_order_relaxed);
     ++t_launches;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Clusters of two (the CTA-pair GEMMs).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pair(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                        Args&&... args)
+{
+    return launch_cluster(kernel, 2, grid, block, smem, st, std::forward<Args>(args)...);
 }
 
 // How many clusters of two CTAs of `kernel` can be resident at once (0 on error).
@@ -170,7 +182,13 @@ int device_setup(DeviceState** out)
                 cudaFuncSetAttribute(grouped_gemm_kernel<MODE_DOWN, true>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmemBytes) != cudaSuccess ||
                 cudaFuncSetAttribute(grouped_gemm_kernel<MODE_FUSED, true>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmemBytes) != cudaSuccess)
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmemBytes) != cudaSuccess ||
+                cudaFuncSetAttribute(int8_gemm_kernel<I8_SINGLE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kI8SmemBytes) != cudaSuccess ||
+                cudaFuncSetAttribute(int8_gemm_kernel<I8_PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kI8SmemBytes) != cudaSuccess ||
+                cudaFuncSetAttribute(int8_gemm_kernel<I8_SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kI8SmemBytes) != cudaSuccess)
                 return MOE_ERR_CUDA;
             // CTA pairs: a grid of exactly the clusters that fit at once, so the
             // persistent pairs all start together (the same count for every mode)
@@ -186,6 +204,7 @@ int device_setup(DeviceState** out)
             pc8 = std::min(pc8, max_pair_clusters(grouped_gemm_fp8_kernel<FP8_DOWN, true, true>, kFp8SmemBytes,
                                                   kFp8Threads));
             st.fp8_pair_grid = 2 * std::min(pc8, sms / 2);
+            st.i8_pair_grid = 2 * std::min(max_pair_clusters(int8_gemm_kernel<I8_PAIR>, kI8SmemBytes), sms / 2);
             if (!g_encode) {
                 cudaDriverEntryPointQueryResult q;
                 void* fn = nullptr;
@@ -1347,3 +1366,325 @@ extern "C" int moe_permute_noalloc(const int32_t* topk_idx, const moe_bf16* x, i
                        perm, inv_perm, reinterpret_cast<bf16*>(xp), err, scratch, nullptr, 0, 0, 0, dev->sm_count,
                        st, kPlanSingle);
 }
+
+// ---------------------------------------------------------------- norms, int8 products, sorted rows
+namespace {
+
+// Warps of a row and rows of a CTA for a forward row kernel.  Few rows: one vector a
+// thread, the shortest path from load to store; from two rows an SM on: four
+// vectors a thread, more bytes in flight a thread and fewer warps to join.
+RowShape norm_shape(int64_t T, int d, int sms)
+{
+    const int nvec = d / 8;
+    int vpt = T >= 2 * (int64_t)sms ? 4 : 1;
+    while (row_warps(nvec, vpt) > 32) vpt *= 2;
+    return row_shape(nvec, vpt);
+}
+
+template <int OUT>
+int run_norm(const NormArgs& a, int sms, cudaStream_t st)
+{
+    const RowShape s = norm_shape(a.T, a.d, sms);
+    const dim3 grid((unsigned)((a.T + s.groups - 1) / s.groups)), block(s.warps * s.groups * 32);
+    auto kernel = s.vpt == 1 ? rmsnorm_kernel<OUT, 1> : s.vpt == 2 ? rmsnorm_kernel<OUT, 2> : rmsnorm_kernel<OUT, 4>;
+    return status_of(launch(kernel, grid, block, 0, st, a, s.warps));
+}
+
+// Host checks shared by the three forms of the norm.
+int check_norm(const void* x, const void* residual, const void* weight, int64_t T, int64_t d, float eps,
+               const void* xsum, const void* y, int64_t multiple)
+{
+    if (T < 0 || T >= (int64_t(1) << 31) || d <= 0 || d > kNormMaxD) return MOE_ERR_ARG;
+    if (!(eps > 0.f) || eps > 3.4e38f) return MOE_ERR_ARG;
+    if (d % multiple != 0) return MOE_ERR_ALIGN;
+    if (T == 0) return MOE_OK;
+    if (!x || !weight || (!residual) != (!xsum)) return MOE_ERR_ARG;
+    if (!al16(x) || !al16(weight) || !al16(residual) || !al16(xsum) || !al16(y)) return MOE_ERR_ALIGN;
+    return MOE_OK;
+}
+
+template <int OUT>
+int norm_entry(const moe_bf16* x, const moe_bf16* residual, const moe_bf16* weight, int64_t T, int64_t d, float eps,
+               moe_bf16* xsum, moe_bf16* y, uint8_t* q, float* scale, void* stream)
+{
+    int rc = check_norm(x, residual, weight, T, d, eps, xsum, y, OUT == NORM_FP8 ? 128 : 64);
+    if (rc) return rc;
+    if (T == 0) return MOE_OK;
+    if (OUT == NORM_BF16 ? !y : (!q || !scale)) return MOE_ERR_ARG;
+    if (OUT != NORM_BF16 && !al16(q)) return MOE_ERR_ALIGN;
+    DeviceState* dev;
+    if ((rc = device_setup(&dev))) return rc;
+    NormArgs a{};
+    a.x = reinterpret_cast<const bf16*>(x);
+    a.residual = reinterpret_cast<const bf16*>(residual);
+    a.weight = reinterpret_cast<const bf16*>(weight);
+    a.xsum = reinterpret_cast<bf16*>(xsum);
+    a.y = reinterpret_cast<bf16*>(y);
+    a.q = q;
+    a.scale = scale;
+    a.T = T;
+    a.d = (int)d;
+    a.eps = eps;
+    return run_norm<OUT>(a, dev->sm_count, as_stream(stream));
+}
+
+constexpr PlanShape kPlanI8{kTileRows, 64, 128, 16, 0, kTilesCap};
+constexpr PlanShape kPlanI8Pair{kTileRows, 128, 256, 32, 1, kTilesCap};
+
+int check_int8(int64_t N, int64_t K)
+{
+    if (N <= 0 || K <= 0 || N >= (int64_t(1) << 31) || K > kI8MaxK) return MOE_ERR_ARG;
+    if (N % 64 != 0 || K % 64 != 0) return MOE_ERR_ALIGN;
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_rmsnorm(const moe_bf16* x, const moe_bf16* residual, const moe_bf16* weight, int64_t T, int64_t d, float eps,
+                moe_bf16* xsum, moe_bf16* y, void* stream)
+{
+    return norm_entry<NORM_BF16>(x, residual, weight, T, d, eps, xsum, y, nullptr, nullptr, stream);
+}
+
+int moe_rmsnorm_fp8(const moe_bf16* x, const moe_bf16* residual, const moe_bf16* weight, int64_t T, int64_t d,
+                    float eps, moe_bf16* xsum, moe_bf16* y, uint8_t* q, float* scales, void* stream)
+{
+    return norm_entry<NORM_FP8>(x, residual, weight, T, d, eps, xsum, y, q, scales, stream);
+}
+
+int moe_rmsnorm_int8(const moe_bf16* x, const moe_bf16* residual, const moe_bf16* weight, int64_t T, int64_t d,
+                     float eps, moe_bf16* xsum, moe_bf16* y, int8_t* q, float* scale, void* stream)
+{
+    return norm_entry<NORM_INT8>(x, residual, weight, T, d, eps, xsum, y, reinterpret_cast<uint8_t*>(q), scale,
+                                 stream);
+}
+
+int moe_rmsnorm_backward_workspace_size(int64_t T, int64_t d, size_t* bytes)
+{
+    if (!bytes || T < 0 || T >= (int64_t(1) << 31) || d <= 0 || d > kNormMaxD) return MOE_ERR_ARG;
+    *bytes = align_up((size_t)norm_grad_groups(T, (int)d) * d * 4, 256);
+    return MOE_OK;
+}
+
+int moe_rmsnorm_backward(const moe_bf16* dy, const moe_bf16* xsum, const moe_bf16* weight, const moe_bf16* dxsum,
+                         int64_t T, int64_t d, float eps, moe_bf16* dx, float* dweight, void* ws, size_t ws_bytes,
+                         void* stream)
+{
+    if (T < 0 || T >= (int64_t(1) << 31) || d <= 0 || d > kNormMaxD) return MOE_ERR_ARG;
+    if (!(eps > 0.f) || eps > 3.4e38f) return MOE_ERR_ARG;
+    if (d % 64 != 0) return MOE_ERR_ALIGN;
+    if (!dweight) return MOE_ERR_ARG;
+    cudaStream_t st = as_stream(stream);
+    DeviceState* dev;
+    int rc;
+    if (T == 0) {   // a sum over no rows
+        if ((rc = device_setup(&dev))) return rc;
+        return status_of(cudaMemsetAsync(dweight, 0, (size_t)d * 4, st));
+    }
+    if (!dy || !xsum || !weight || !dx || !ws) return MOE_ERR_ARG;
+    if (!al16(dy) || !al16(xsum) || !al16(weight) || !al16(dxsum) || !al16(dx) || !al16(ws)) return MOE_ERR_ALIGN;
+    const int64_t groups = norm_grad_groups(T, (int)d);
+    if (ws_bytes < (size_t)groups * d * 4) return MOE_ERR_WS;
+    if ((rc = device_setup(&dev))) return rc;
+    const RowShape s = norm_grad_shape((int)d);
+    NormGradArgs a{};
+    a.dy = reinterpret_cast<const bf16*>(dy);
+    a.s = reinterpret_cast<const bf16*>(xsum);
+    a.weight = reinterpret_cast<const bf16*>(weight);
+    a.dxsum = reinterpret_cast<const bf16*>(dxsum);
+    a.dx = reinterpret_cast<bf16*>(dx);
+    a.partials = static_cast<float*>(ws);
+    a.T = T;
+    a.d = (int)d;
+    a.eps = eps;
+    auto kernel = s.vpt == 2 ? rmsnorm_grad_kernel<2> : rmsnorm_grad_kernel<4>;
+    if (launch(kernel, dim3((unsigned)(groups / s.groups)), dim3(s.warps * s.groups * 32), 0, st, a, s.warps) !=
+        cudaSuccess)
+        return MOE_ERR_CUDA;
+    return status_of(launch(norm_dw_kernel, dim3((unsigned)((d + 31) / 32)), dim3(256), 0, st,
+                            (const float*)a.partials, groups, (int)d, dweight));
+}
+
+int moe_quantize_int8_rows(const moe_bf16* x, int64_t rows, int64_t cols, int8_t* q, float* scale, void* stream)
+{
+    if (rows < 0 || rows >= (int64_t(1) << 31) || cols <= 0 || cols > kNormMaxD) return MOE_ERR_ARG;
+    if (cols % 64 != 0) return MOE_ERR_ALIGN;
+    if (rows == 0) return MOE_OK;
+    if (!x || !q || !scale) return MOE_ERR_ARG;
+    if (!al16(x) || !al16(q)) return MOE_ERR_ALIGN;
+    DeviceState* dev;
+    int rc;
+    if ((rc = device_setup(&dev))) return rc;
+    NormArgs a{};
+    a.x = reinterpret_cast<const bf16*>(x);
+    a.q = reinterpret_cast<uint8_t*>(q);
+    a.scale = scale;
+    a.T = rows;
+    a.d = (int)cols;
+    return run_norm<NORM_INT8>(a, dev->sm_count, as_stream(stream));
+}
+
+int moe_gemm_int8(const int8_t* xq, const float* sx, const int8_t* Wq, const float* sw, int64_t T, int64_t K,
+                  int64_t N, moe_bf16* out, void* ws, size_t ws_bytes, void* stream)
+{
+    int rc = check_int8(N, K);
+    if (rc) return rc;
+    if (T < 0 || T >= (int64_t(1) << 31)) return MOE_ERR_ARG;
+    if (T == 0) return MOE_OK;
+    if (!xq || !sx || !Wq || !sw || !out || !ws) return MOE_ERR_ARG;
+    if (!al16(xq) || !al16(sx) || !al16(Wq) || !al16(sw) || !al16(out) || !al16(ws)) return MOE_ERR_ALIGN;
+    if (ws_bytes < 256) return MOE_ERR_WS;   // the error word
+    DeviceState* dev;
+    if ((rc = device_setup(&dev))) return rc;
+    cudaStream_t st = as_stream(stream);
+    CUtensorMap ma, mb16, mb64;
+    if (!make_map_u8(&ma, Wq, K, N, 128) || !make_map_u8(&mb16, xq, K, T, 16) || !make_map_u8(&mb64, xq, K, T, 64))
+        return MOE_ERR_CUDA;
+    Int8Args a{};
+    a.T = (int)T;
+    a.units = (int)((T + kTileRows - 1) / kTileRows);
+    a.chunk = (int)((T + a.units - 1) / a.units + 15) / 16 * 16;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.sx = sx;
+    a.sw = sw;
+    a.out = reinterpret_cast<bf16*>(out);
+    a.err = static_cast<uint32_t*>(ws);
+    const int64_t tiles = (N + 127) / 128 * a.units;
+    if (tiles >= (int64_t(1) << 31)) return MOE_ERR_ARG;
+    return status_of(launch(int8_gemm_kernel<I8_SINGLE>, dim3((unsigned)std::min<int64_t>(tiles, dev->sm_count)),
+                            dim3(kGemmThreads), kI8SmemBytes, st, ma, mb16, mb64, a));
+}
+
+int moe_grouped_gemm_int8(const int8_t* xpq, const float* sxp, const int32_t* counts, const int32_t* offsets,
+                          const int8_t* Wq, const float* sw, int64_t T, int64_t K, int64_t N, int64_t E, int64_t k,
+                          moe_bf16* out, void* ws, size_t ws_bytes, void* stream)
+{
+    int rc = check_sizes(T, 64, E, k);
+    if (rc) return rc;
+    if ((rc = check_int8(N, K))) return rc;
+    if (E * N >= (int64_t(1) << 31)) return MOE_ERR_ARG;
+    if (T == 0) return MOE_OK;
+    if (!xpq || !sxp || !counts || !offsets || !Wq || !sw || !out || !ws) return MOE_ERR_ARG;
+    if (!al16(xpq) || !al16(sxp) || !al16(Wq) || !al16(sw) || !al16(out) || !al16(ws)) return MOE_ERR_ALIGN;
+    const WsLayout L = ws_layout(T, 0, 0, E, k, 0);
+    if (ws_bytes < L.ctrl_end) return MOE_ERR_WS;
+    DeviceState* dev;
+    if ((rc = device_setup(&dev))) return rc;
+    cudaStream_t st = as_stream(stream);
+    int32_t* plan = at<int32_t>(ws, L.plan);
+    const int64_t P = T * k;
+    const PlanShape ps = kPlanI8;
+    if (launch(plan_kernel, dim3(1), dim3(1024), 0, st, counts, offsets, (int)E, plan, 0, (int)N, 0, 0, ps) !=
+        cudaSuccess)
+        return MOE_ERR_CUDA;
+    CUtensorMap ma, mb16, mb64;
+    if (!make_map_u8(&ma, Wq, K, E * N, 128) || !make_map_u8(&mb16, xpq, K, P, 16) || !make_map_u8(&mb64, xpq, K, P, 64))
+        return MOE_ERR_CUDA;
+    Int8Args a{};
+    a.plan = plan;
+    a.T = (int)P;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.sx = sxp;
+    a.sw = sw;
+    a.out = reinterpret_cast<bf16*>(out);
+    a.err = at<uint32_t>(ws, L.err);
+    return status_of(launch(int8_gemm_kernel<I8_SINGLE>, dim3(dev->sm_count), dim3(kGemmThreads), kI8SmemBytes, st,
+                            ma, mb16, mb64, a));
+}
+
+int moe_permute_int8(const int32_t* topk_idx, const int8_t* xq, const float* sx, int64_t T, int64_t d, int64_t E,
+                     int64_t k, int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv_perm, int8_t* xpq,
+                     float* sxp, void* ws, size_t ws_bytes, void* stream)
+{
+    int rc = check_sizes(T, d, E, k);
+    if (rc) return rc;
+    if (T == 0) return MOE_OK;
+    if (!topk_idx || !xq || !sx || !counts || !offsets || !perm || !inv_perm || !xpq || !sxp || !ws)
+        return MOE_ERR_ARG;
+    if (!al16(xq) || !al16(xpq) || !al16(ws)) return MOE_ERR_ALIGN;
+    const WsLayout L = ws_layout(T, 0, 0, E, k, 0);
+    if (ws_bytes < L.ctrl_end) return MOE_ERR_WS;
+    DeviceState* dev;
+    if ((rc = device_setup(&dev))) return rc;
+    cudaStream_t st = as_stream(stream);
+    uint32_t* err = at<uint32_t>(ws, L.err);
+    if (T * k <= kSmallPairs) {
+        if (launch(permute_small_kernel, dim3(1), dim3(1024), 0, st, topk_idx, (int)(T * k), (int)E, counts, offsets,
+                   perm, inv_perm, (int32_t*)nullptr, 0, 0, 0, 0, kPlanSingle, err) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    } else if ((rc = run_permute(topk_idx, nullptr, (int)T, (int)d, (int)E, (int)k, counts, offsets, perm, inv_perm,
+                                 nullptr, err, at<int32_t>(ws, L.block_counts), nullptr, 0, 0, 0, dev->sm_count, st,
+                                 kPlanSingle))) {
+        return rc;
+    }
+    return status_of(launch(gather_rows_int8_kernel, dim3(gather_blocks(T, (int)(d / 16), dev->sm_count)), dim3(256),
+                            0, st, reinterpret_cast<const uint8_t*>(xq), sx, (const int32_t*)inv_perm, T, (int)k,
+                            (int)d, reinterpret_cast<uint8_t*>(xpq), sxp));
+}
+
+// Sizes of the entry points that only read a permutation.
+static int check_pairs(int64_t T, int64_t k, int64_t d)
+{
+    if (T < 0 || k < 1 || k > kMaxTopK || d <= 0 || d >= (int64_t(1) << 31) || T * k >= (int64_t(1) << 31))
+        return MOE_ERR_ARG;
+    return d % 64 != 0 ? MOE_ERR_ALIGN : MOE_OK;
+}
+
+static int run_return(const bf16* rows, const int32_t* inv_perm, const float* gates, const bf16* add, int64_t T,
+                      int64_t k, int64_t d, bf16* out, void* stream)
+{
+    DeviceState* dev;
+    int rc;
+    if ((rc = device_setup(&dev))) return rc;
+    const int nvec = (int)(d / 8), threads = 64;
+    const int gy = std::min((nvec + threads - 1) / threads, 65535);
+    return status_of(launch(return_rows_kernel, dim3((unsigned)T, gy), dim3(threads), 0, as_stream(stream), rows,
+                            inv_perm, gates, add, T, (int)k, (int)d, out));
+}
+
+int moe_combine_weighted(const moe_bf16* y_p, const int32_t* inv_perm, const float* topk_w,
+                         const moe_bf16* shared_out, int64_t T, int64_t k, int64_t d, moe_bf16* out, void* stream)
+{
+    int rc = check_pairs(T, k, d);
+    if (rc) return rc;
+    if (T == 0) return MOE_OK;
+    if (!y_p || !inv_perm || !topk_w || !out) return MOE_ERR_ARG;
+    if (!al16(y_p) || !al16(out) || !al16(shared_out)) return MOE_ERR_ALIGN;
+    return run_return(reinterpret_cast<const bf16*>(y_p), inv_perm, topk_w, reinterpret_cast<const bf16*>(shared_out),
+                      T, k, d, reinterpret_cast<bf16*>(out), stream);
+}
+
+int moe_combine_weighted_backward(const moe_bf16* dout, const moe_bf16* y_p, const int32_t* inv_perm,
+                                  const float* topk_w, int64_t T, int64_t k, int64_t d, moe_bf16* dy_p, float* dw,
+                                  void* stream)
+{
+    int rc = check_pairs(T, k, d);
+    if (rc) return rc;
+    if (T == 0) return MOE_OK;
+    if (!dout || !y_p || !inv_perm || !topk_w || !dy_p || !dw) return MOE_ERR_ARG;
+    if (!al16(dout) || !al16(y_p) || !al16(dy_p)) return MOE_ERR_ALIGN;
+    DeviceState* dev;
+    if ((rc = device_setup(&dev))) return rc;
+    const int threads = (int)std::min<int64_t>(256, (d / 8 + 31) / 32 * 32);
+    return status_of(launch(return_rows_grad_kernel, dim3((unsigned)T), dim3(threads), 0, as_stream(stream),
+                            reinterpret_cast<const bf16*>(dout), reinterpret_cast<const bf16*>(y_p), inv_perm, topk_w,
+                            T, (int)k, (int)d, reinterpret_cast<bf16*>(dy_p), dw));
+}
+
+int moe_permute_backward(const moe_bf16* dxp, const int32_t* inv_perm, const moe_bf16* addend, int64_t T, int64_t k,
+                         int64_t d, moe_bf16* dx, void* stream)
+{
+    int rc = check_pairs(T, k, d);
+    if (rc) return rc;
+    if (T == 0) return MOE_OK;
+    if (!dxp || !inv_perm || !dx) return MOE_ERR_ARG;
+    if (!al16(dxp) || !al16(dx) || !al16(addend)) return MOE_ERR_ALIGN;
+    return run_return(reinterpret_cast<const bf16*>(dxp), inv_perm, nullptr, reinterpret_cast<const bf16*>(addend), T,
+                      k, d, reinterpret_cast<bf16*>(dx), stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,435 @@
+// norm.cuh -- the residual's addition with a root-mean-square norm, its result
+// in bf16, in e4m3 with 1 x 128 scales or in int8 with one scale a row; its
+// gradient; and the int8 row quantiser.
+//
+//   s    = bf16(x + r)                         the residual stream (r absent: s = x)
+//   rstd = 1 / sqrt(mean(s^2) + eps)
+//   y    = bf16(s * rstd * w)
+//   q    = the codes of y: those of moe_quantize_fp8_rows (1 x 128 blocks) or of
+//          moe_quantize_int8_rows (one scale a row), bit for bit
+//
+// Roundings: s once (the stream is kept in bf16 and the norm is of what is
+// kept), y once, and the codes are taken from the rounded y, so that a router
+// that reads y and experts that read q see the same row.  Squares, means and
+// the gradient's sums are fp32.
+//
+// Bound: HBM.  Every input is read once and every output written once: a row
+// stays in the registers of one group of warps between the reduction and the
+// normalisation.
+#pragma once
+
+#include "common.cuh"
+#include "fp8.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+
+constexpr int kNormMaxD = 32768;             // 1024 threads x 4 vectors of 8
+constexpr int NORM_BF16 = 0, NORM_FP8 = 1, NORM_INT8 = 2;
+
+// How rows are laid over a CTA: a row belongs to a group of `warps` warps whose
+// threads hold `vpt` 16-byte vectors each; `groups` rows share a CTA.
+struct RowShape {
+    int vpt, warps, groups;
+};
+
+__host__ __device__ inline int row_warps(int nvec, int vpt) { return (nvec + 32 * vpt - 1) / (32 * vpt); }
+
+// The layout of d / 8 vectors at `vpt` a thread: short rows share a CTA, up to 8 warps.
+__host__ __device__ inline RowShape row_shape(int nvec, int vpt)
+{
+    RowShape s{vpt, row_warps(nvec, vpt), 1};
+    while (s.groups < 8 && s.warps * s.groups * 2 <= 8) s.groups *= 2;
+    return s;
+}
+
+struct f8 {
+    float v[8];
+};
+
+__device__ __forceinline__ f8 unpack8(const uint4& u)
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    f8 r;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        r.v[2 * i] = __uint_as_float(w[i] << 16);
+        r.v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+    return r;
+}
+
+__device__ __forceinline__ uint4 pack8(const f8& f)
+{
+    uint4 u;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(f.v[2 * i], f.v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    return u;
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ uint32_t warp_umax(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
+
+// Barrier over one group of warps (id 1.. for group 0..); a group of one warp needs no hardware barrier.
+__device__ __forceinline__ void group_barrier(int group, int warps)
+{
+    if (warps == 1) __syncwarp();
+    else ptx::named_barrier(1 + group, warps * 32);
+}
+
+// Sum over the group's threads, in the same order in every thread.  `slot` is
+// this group's own scratch of `warps` floats, not read by an earlier reduction
+// that a warp of the group may still be in.
+__device__ __forceinline__ float group_sum(float v, float* slot, int group, int warps)
+{
+    v = warp_sum(v);
+    if (warps == 1) return v;
+    const int lane = threadIdx.x & 31, w = (int)(threadIdx.x >> 5) - group * warps;
+    if (lane == 0) slot[w] = v;
+    group_barrier(group, warps);
+    return warp_sum(lane < warps ? slot[lane] : 0.f);
+}
+
+__device__ __forceinline__ uint32_t group_umax(uint32_t v, uint32_t* slot, int group, int warps)
+{
+    v = warp_umax(v);
+    if (warps == 1) return v;
+    const int lane = threadIdx.x & 31, w = (int)(threadIdx.x >> 5) - group * warps;
+    if (lane == 0) slot[w] = v;
+    group_barrier(group, warps);
+    return warp_umax(lane < warps ? slot[lane] : 0u);
+}
+
+// The magnitude bits of the largest of 8 bf16 values (a NaN ranks above infinity), as fp32 bits.
+__device__ __forceinline__ uint32_t amax_bits8(const uint4& u)
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) m = max(m, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
+    return m;
+}
+
+// ---------------------------------------------------------------- int8 codes
+// One scale a row: scale = amax / 127, code = round(v * (127 / amax)) to even.
+// A row whose largest magnitude is below 2^-100 counts as all zero (scale 1,
+// codes 0): amax / 127 and 127 / amax are then both normal fp32 numbers.  A row
+// that holds a NaN or an infinity gets the scale NaN, so that it stays visible
+// in every product made of it.
+struct Int8Scale {
+    float scale, inv;
+};
+
+__device__ __forceinline__ Int8Scale int8_scale(uint32_t amax_bits)
+{
+    if (amax_bits >= 0x7F800000u) return {__uint_as_float(0x7FC00000u), 0.f};
+    const float amax = __uint_as_float(amax_bits);
+    if (amax < 7.888609052210118e-31f) return {1.f, 0.f};   // 2^-100
+    return {amax / 127.f, 127.f / amax};
+}
+
+__device__ __forceinline__ uint2 int8_codes8(const uint4& u, float inv)
+{
+    const f8 f = unpack8(u);
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        // |v * inv| <= 127 (1 + 2^-23): rounds to at most 127.  inv = 0 (a NaN or
+        // infinite row) makes 0 or NaN, and a NaN converts to code 0.
+        const int c = __float2int_rn(f.v[i] * inv);
+        w[i >> 2] |= (uint32_t)(c & 0xFF) << (8 * (i & 3));
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// ---------------------------------------------------------------- e4m3 codes
+// 8 values of a 1 x 128 block spread over 16 consecutive lanes: the block's
+// exponent (the rule of the row quantiser in fp8.cuh) and this lane's codes.
+__device__ __forceinline__ int e4m3_block_exp(const uint4& u)
+{
+    const f8 f = unpack8(u);
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) a = fmaxf(a, fabsf(f.v[i]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    return fp8_scale_exp(a);
+}
+
+__device__ __forceinline__ uint2 e4m3_codes8(const uint4& u, int e)
+{
+    const f8 f = unpack8(u);
+    const float m = pow2f(-e);   // v * 2^-e: the same single rounding as ldexpf(v, -e)
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint32_t p = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(f.v[2 * i] * m, f.v[2 * i + 1] * m),
+                                                              __NV_SATFINITE, __NV_E4M3);
+        w[i >> 1] |= p << (16 * (i & 1));
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// ---------------------------------------------------------------- forward
+struct NormArgs {
+    const bf16* x;
+    const bf16* residual;   // may be null
+    const bf16* weight;     // null (the int8 row quantiser): y = x, no norm
+    bf16* xsum;             // with residual: may be x or residual (each element is read before it is written)
+    bf16* y;                // may be null when there are codes
+    uint8_t* q;
+    float* scale;           // int8: [T]; e4m3: [T, d / 128]
+    int64_t T;
+    int d;
+    float eps;
+};
+
+// One row a group.  d % 8 == 0 (e4m3: d % 128 == 0).
+template <int OUT, int VPT>
+__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a, int warps)
+{
+    __shared__ float s_sum[32];
+    __shared__ uint32_t s_max[32];
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int gt = warps * 32;                       // threads of a group
+    const int group = (int)threadIdx.x / gt, ti = (int)threadIdx.x - group * gt;
+    const int64_t row = (int64_t)blockIdx.x * ((int)blockDim.x / gt) + group;
+    if (row >= a.T) return;                          // the whole group leaves
+    const int nvec = a.d / 8;
+    const uint4* xr = reinterpret_cast<const uint4*>(a.x + row * a.d);
+    uint4 u[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; i++) {
+        const int v = i * gt + ti;
+        u[i] = v < nvec ? xr[v] : make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (a.residual) {
+        const uint4* rr = reinterpret_cast<const uint4*>(a.residual + row * a.d);
+        uint4 r[VPT];
+#pragma unroll
+        for (int i = 0; i < VPT; i++) {
+            const int v = i * gt + ti;
+            r[i] = v < nvec ? rr[v] : make_uint4(0u, 0u, 0u, 0u);
+        }
+        uint4* sr = reinterpret_cast<uint4*>(a.xsum + row * a.d);
+#pragma unroll
+        for (int i = 0; i < VPT; i++) {
+            const int v = i * gt + ti;
+            f8 s = unpack8(u[i]);
+            const f8 t = unpack8(r[i]);
+#pragma unroll
+            for (int j = 0; j < 8; j++) s.v[j] += t.v[j];
+            u[i] = pack8(s);
+            if (v < nvec) sr[v] = u[i];
+        }
+    }
+    if (a.weight) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; i++) {
+            const f8 s = unpack8(u[i]);
+#pragma unroll
+            for (int j = 0; j < 8; j++) ss = fmaf(s.v[j], s.v[j], ss);
+        }
+        ss = group_sum(ss, s_sum + group * warps, group, warps);
+        const float rstd = rsqrtf(ss / (float)a.d + a.eps);
+        const uint4* wr = reinterpret_cast<const uint4*>(a.weight);
+#pragma unroll
+        for (int i = 0; i < VPT; i++) {
+            const int v = i * gt + ti;
+            f8 s = unpack8(u[i]);
+            const f8 w = unpack8(v < nvec ? __ldg(wr + v) : make_uint4(0u, 0u, 0u, 0u));
+#pragma unroll
+            for (int j = 0; j < 8; j++) s.v[j] = s.v[j] * rstd * w.v[j];
+            u[i] = pack8(s);
+        }
+        // past the row's end a NaN rstd would leave NaN here: those vectors are zero
+#pragma unroll
+        for (int i = 0; i < VPT; i++)
+            if (i * gt + ti >= nvec) u[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (OUT == NORM_BF16 || a.y) {
+            uint4* yr = reinterpret_cast<uint4*>(a.y + row * a.d);
+#pragma unroll
+            for (int i = 0; i < VPT; i++) {
+                const int v = i * gt + ti;
+                if (v < nvec) yr[v] = u[i];
+            }
+        }
+    }
+    if (OUT == NORM_FP8) {
+        uint2* qr = reinterpret_cast<uint2*>(a.q + row * a.d);
+#pragma unroll
+        for (int i = 0; i < VPT; i++) {
+            const int v = i * gt + ti;
+            const int e = e4m3_block_exp(u[i]);
+            if (v < nvec) {
+                qr[v] = e4m3_codes8(u[i], e);
+                if ((ti & 15) == 0) a.scale[row * (a.d / 128) + (v >> 4)] = pow2f(e);
+            }
+        }
+    } else if (OUT == NORM_INT8) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < VPT; i++) m = max(m, amax_bits8(u[i]));
+        m = group_umax(m, s_max + group * warps, group, warps);
+        const Int8Scale sc = int8_scale(m);
+        uint2* qr = reinterpret_cast<uint2*>(a.q + row * a.d);
+#pragma unroll
+        for (int i = 0; i < VPT; i++) {
+            const int v = i * gt + ti;
+            if (v < nvec) qr[v] = int8_codes8(u[i], sc.inv);
+        }
+        if (ti == 0) a.scale[row] = sc.scale;
+    }
+}
+
+// ---------------------------------------------------------------- gradient
+// With n = s * rstd, g = dy * w, m = mean(g * n):
+//   ds = (g - n * m) * rstd (+ dxsum, the stream's own gradient)   -> dx, bf16
+//   dw = sum over rows of dy * n                                   -> fp32
+// rstd is formed again from s, which is read anyway.  Each group walks the rows
+// group, group + groups, ... and keeps its columns' dw in registers; it writes
+// them once to partials[group][d], and norm_dw_kernel adds the groups in a
+// fixed order: no atomics, the same bits in every run.
+struct NormGradArgs {
+    const bf16* dy;
+    const bf16* s;
+    const bf16* weight;
+    const bf16* dxsum;      // may be null
+    bf16* dx;               // may be dy or dxsum
+    float* partials;        // [groups, d]
+    int64_t T;
+    int d;
+    float eps;
+};
+
+constexpr int kNormGradCtas = 296;   // two a B200 SM; fixed, so that the workspace and every bit follow from the sizes
+
+// Layout of the gradient's rows: 2 vectors a thread up to d = 16384 (the
+// columns' dw, 8 floats a vector, stay in registers), 4 above.
+__host__ __device__ inline RowShape norm_grad_shape(int d) { return row_shape(d / 8, d <= 16384 ? 2 : 4); }
+
+__host__ __device__ inline int64_t norm_grad_groups(int64_t T, int d)
+{
+    const RowShape s = norm_grad_shape(d);
+    const int64_t ctas = (T + s.groups - 1) / s.groups;
+    return (ctas < kNormGradCtas ? ctas : kNormGradCtas) * s.groups;
+}
+
+template <int VPT>
+__global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const NormGradArgs a, int warps)
+{
+    __shared__ float s_red[2][2][32];
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int gt = warps * 32;
+    const int per_cta = (int)blockDim.x / gt;
+    const int group = (int)threadIdx.x / gt, ti = (int)threadIdx.x - group * gt;
+    const int64_t stride = (int64_t)gridDim.x * per_cta, g0 = (int64_t)blockIdx.x * per_cta + group;
+    const int nvec = a.d / 8;
+    float dw[VPT][8];
+    uint4 w[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; i++) {
+        const int v = i * gt + ti;
+        w[i] = v < nvec ? __ldg(reinterpret_cast<const uint4*>(a.weight) + v) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int j = 0; j < 8; j++) dw[i][j] = 0.f;
+    }
+    int par = 0;
+    for (int64_t row = g0; row < a.T; row += stride, par ^= 1) {
+        uint4 us[VPT], ug[VPT], ur[VPT];
+#pragma unroll
+        for (int i = 0; i < VPT; i++) {
+            const int v = i * gt + ti;
+            const bool in = v < nvec;
+            us[i] = in ? reinterpret_cast<const uint4*>(a.s + row * a.d)[v] : make_uint4(0u, 0u, 0u, 0u);
+            ug[i] = in ? reinterpret_cast<const uint4*>(a.dy + row * a.d)[v] : make_uint4(0u, 0u, 0u, 0u);
+            ur[i] = in && a.dxsum ? reinterpret_cast<const uint4*>(a.dxsum + row * a.d)[v] : make_uint4(0u, 0u, 0u, 0u);
+        }
+        float ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; i++) {
+            const f8 s = unpack8(us[i]), g = unpack8(ug[i]), wf = unpack8(w[i]);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                ss = fmaf(s.v[j], s.v[j], ss);
+                dot = fmaf(g.v[j] * wf.v[j], s.v[j], dot);
+            }
+        }
+        // both sums through one barrier; the scratch alternates from row to row
+        ss = warp_sum(ss);
+        dot = warp_sum(dot);
+        if (warps > 1) {
+            const int lane = threadIdx.x & 31, wi = (int)(threadIdx.x >> 5);
+            if (lane == 0) {
+                s_red[par][0][wi] = ss;
+                s_red[par][1][wi] = dot;
+            }
+            group_barrier(group, warps);
+            ss = warp_sum(lane < warps ? s_red[par][0][group * warps + lane] : 0.f);
+            dot = warp_sum(lane < warps ? s_red[par][1][group * warps + lane] : 0.f);
+        }
+        const float rstd = rsqrtf(ss / (float)a.d + a.eps);
+        const float m = dot * rstd / (float)a.d;      // mean(g * n)
+#pragma unroll
+        for (int i = 0; i < VPT; i++) {
+            const int v = i * gt + ti;
+            const f8 s = unpack8(us[i]), g = unpack8(ug[i]), wf = unpack8(w[i]), r = unpack8(ur[i]);
+            f8 o;
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const float n = s.v[j] * rstd;
+                o.v[j] = (g.v[j] * wf.v[j] - n * m) * rstd + r.v[j];
+                dw[i][j] = fmaf(g.v[j], n, dw[i][j]);
+            }
+            if (v < nvec) reinterpret_cast<uint4*>(a.dx + row * a.d)[v] = pack8(o);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; i++) {
+        const int v = i * gt + ti;
+        if (v < nvec) {
+            float4* p = reinterpret_cast<float4*>(a.partials + g0 * a.d) + 2 * v;
+            p[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+            p[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+        }
+    }
+}
+
+// dweight[c] = sum over groups of partials[g][c], in a fixed order: a CTA of 256
+// threads takes 32 columns, 8 threads a column each every 8th group, then those
+// 8 sums in order.
+__global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ partials, int64_t groups, int d,
+                                                      float* __restrict__ dweight)
+{
+    __shared__ float s_part[8][33];
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int cx = threadIdx.x & 31, gy = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + cx;
+    float acc = 0.f;
+    if (c < d)
+        for (int64_t g = gy; g < groups; g += 8) acc += partials[g * d + c];
+    s_part[gy][cx] = acc;
+    __syncthreads();
+    if (gy == 0 && c < d) {
+        float t = s_part[0][cx];
+#pragma unroll
+        for (int i = 1; i < 8; i++) t += s_part[i][cx];
+        dweight[c] = t;
+    }
+}
+
+}  // namespace moe

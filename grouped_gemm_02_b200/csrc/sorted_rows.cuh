@@ -1,0 +1,165 @@
+// sorted_rows.cuh -- rows sorted by expert and back with the gates applied, and
+// the gradient of both.
+//
+//   sort        xpq[pos] = xq[t], sxp[pos] = sx[t]           pos = inv_perm[t k + j]
+//   back        out[t]   = sum_j w[t, j] y_p[pos] (+ shared[t])
+//   back'       dy_p[pos] = w[t, j] dout[t],   dw[t, j] = <dout[t], y_p[pos]>
+//   sort'       dx[t]    = sum_j dxp[pos] (+ addend[t])
+//
+// A pair without a position (inv_perm outside [0, T k): its expert id was out
+// of range) adds nothing, gets dw = 0, and no row is written for it.  Sums are
+// fp32 in ascending j (a dot product in a fixed tree), no atomics; rows are
+// rounded to bf16 once.
+//
+// Bound: HBM (2 P d bytes a pass over the sorted rows).  All kernels walk tokens
+// in order, so the token's own row is read or written once for its k pairs.
+#pragma once
+
+#include "common.cuh"
+#include "norm.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+
+// Position of pair q, or -1 where it has none.
+__device__ __forceinline__ int pair_pos(const int32_t* inv_perm, int64_t q, int64_t P)
+{
+    const int pos = __ldg(inv_perm + q);
+    return (pos >= 0 && pos < P) ? pos : -1;
+}
+
+// ---------------------------------------------------------------- sort (int8 rows with a scale each)
+// One warp per (token, 512-byte chunk of the row): a 16-byte vector per lane,
+// then its k stores; the first chunk's warp also writes the scales.
+__global__ void __launch_bounds__(256) gather_rows_int8_kernel(const uint8_t* __restrict__ xq,
+                                                               const float* __restrict__ sx,
+                                                               const int32_t* __restrict__ inv_perm, int64_t T, int k,
+                                                               int d, uint8_t* __restrict__ xpq,
+                                                               float* __restrict__ sxp)
+{
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int nvec = d / 16, nch = (nvec + 31) / 32;
+    const int lane = threadIdx.x & 31;
+    const int64_t items = T * nch, P = T * k;
+    for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 32; w < items;
+         w += (int64_t)gridDim.x * blockDim.x / 32) {
+        const int64_t t = w / nch;
+        const int c = (int)(w - t * nch);
+        const int v = c * 32 + lane;
+        const int mine = lane < k ? pair_pos(inv_perm, t * k + lane, P) : -1;
+        uint4 buf = make_uint4(0u, 0u, 0u, 0u);
+        if (v < nvec) buf = __ldg(reinterpret_cast<const uint4*>(xq + t * d) + v);
+        if (c == 0 && mine >= 0) sxp[mine] = sx[t];
+        for (int j = 0; j < k; j++) {
+            const int pos = __shfl_sync(0xffffffffu, mine, j);
+            if (pos >= 0 && v < nvec) reinterpret_cast<uint4*>(xpq + (int64_t)pos * d)[v] = buf;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- back, and the gradient of sort
+// out[t] = sum_j w[t, j] rows[pos] + add[t]; w null: weights 1.  One thread per
+// 16-byte vector of a token's row, its k loads in flight together.
+__global__ void __launch_bounds__(256) return_rows_kernel(const bf16* __restrict__ rows,
+                                                          const int32_t* __restrict__ inv_perm,
+                                                          const float* __restrict__ gates, const bf16* __restrict__ add,
+                                                          int64_t T, int k, int d, bf16* __restrict__ out)
+{
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int nvec = d / 8;
+    const int64_t P = T * k;
+    const int64_t t = blockIdx.x;
+    int pos[kMaxTopK];
+    float w[kMaxTopK];
+#pragma unroll
+    for (int j = 0; j < kMaxTopK; j++) {
+        pos[j] = j < k ? pair_pos(inv_perm, t * k + j, P) : -1;
+        w[j] = (j < k && gates) ? __ldg(gates + t * k + j) : 1.f;
+    }
+    for (int v = blockIdx.y * blockDim.x + threadIdx.x; v < nvec; v += gridDim.y * blockDim.x) {
+        uint4 u[kMaxTopK];
+#pragma unroll
+        for (int j = 0; j < kMaxTopK; j++)
+            if (pos[j] >= 0) u[j] = __ldg(reinterpret_cast<const uint4*>(rows + (int64_t)pos[j] * d) + v);
+        f8 acc;
+#pragma unroll
+        for (int i = 0; i < 8; i++) acc.v[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < kMaxTopK; j++) {
+            if (pos[j] >= 0) {
+                const f8 r = unpack8(u[j]);
+#pragma unroll
+                for (int i = 0; i < 8; i++) acc.v[i] = fmaf(w[j], r.v[i], acc.v[i]);
+            }
+        }
+        if (add) {
+            const f8 r = unpack8(__ldg(reinterpret_cast<const uint4*>(add + t * d) + v));
+#pragma unroll
+            for (int i = 0; i < 8; i++) acc.v[i] += r.v[i];
+        }
+        reinterpret_cast<uint4*>(out + t * d)[v] = pack8(acc);
+    }
+}
+
+// ---------------------------------------------------------------- gradient of back
+// One CTA per token: its threads hold the token's gradient row a vector at a
+// time, write each pair's scaled copy and add up the k dot products.
+// rows and drows may be the same buffer (no __restrict__, no read-only loads):
+// a vector is read and then written by the same thread.
+__global__ void __launch_bounds__(256) return_rows_grad_kernel(const bf16* __restrict__ dout, const bf16* rows,
+                                                               const int32_t* __restrict__ inv_perm,
+                                                               const float* __restrict__ gates, int64_t T, int k,
+                                                               int d, bf16* drows, float* __restrict__ dgates)
+{
+    __shared__ float s_dot[kMaxTopK][8];
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int nvec = d / 8;
+    const int64_t P = T * k;
+    const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int pos[kMaxTopK];
+    float w[kMaxTopK], dot[kMaxTopK];
+#pragma unroll
+    for (int j = 0; j < kMaxTopK; j++) {
+        pos[j] = j < k ? pair_pos(inv_perm, t * k + j, P) : -1;
+        w[j] = j < k ? __ldg(gates + t * k + j) : 0.f;
+        dot[j] = 0.f;
+    }
+    for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+        uint4 u[kMaxTopK];
+#pragma unroll
+        for (int j = 0; j < kMaxTopK; j++)
+            if (pos[j] >= 0) u[j] = reinterpret_cast<const uint4*>(rows + (int64_t)pos[j] * d)[v];
+        const f8 g = unpack8(__ldg(reinterpret_cast<const uint4*>(dout + t * d) + v));
+#pragma unroll
+        for (int j = 0; j < kMaxTopK; j++) {
+            if (pos[j] >= 0) {
+                const f8 r = unpack8(u[j]);
+                f8 o;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    dot[j] = fmaf(g.v[i], r.v[i], dot[j]);
+                    o.v[i] = w[j] * g.v[i];
+                }
+                reinterpret_cast<uint4*>(drows + (int64_t)pos[j] * d)[v] = pack8(o);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kMaxTopK; j++) {
+        const float s = warp_sum(dot[j]);
+        if (lane == 0) s_dot[j][warp] = s;
+    }
+    __syncthreads();
+    const int warps = (int)(blockDim.x >> 5);
+    if ((int)threadIdx.x < k) {
+        float s = s_dot[threadIdx.x][0];
+        for (int i = 1; i < warps; i++) s += s_dot[threadIdx.x][i];
+        dgates[t * k + threadIdx.x] = s;
+    }
+}
+
+}  // namespace moe

@@ -29,7 +29,10 @@ EXPORTS = ("moe_workspace_size", "moe_workspace_init", "moe_route", "moe_topk", 
            "moe_record_phase_events", "moe_launch_counter", "moe_get_device_error", "moe_clear_device_error",
            "moe_selftest_wait_timeout",
            "moe_status_string", "moe_set_policy", "moe_quantize_fp8_rows", "moe_quantize_fp8_blocks", "moe_workspace_size_fp8",
-           "moe_workspace_tensor_fp8", "moe_layer_forward_fp8", "moe_quantize_fp4_rows", "moe_layer_forward_fp4")
+           "moe_workspace_tensor_fp8", "moe_layer_forward_fp8", "moe_quantize_fp4_rows", "moe_layer_forward_fp4",
+           "moe_rmsnorm", "moe_rmsnorm_fp8", "moe_rmsnorm_int8", "moe_rmsnorm_backward_workspace_size",
+           "moe_rmsnorm_backward", "moe_quantize_int8_rows", "moe_gemm_int8", "moe_grouped_gemm_int8",
+           "moe_permute_int8", "moe_combine_weighted", "moe_combine_weighted_backward", "moe_permute_backward")
 
 
 class MoEError(RuntimeError):
@@ -75,6 +78,18 @@ def lib() -> C.CDLL:
             "moe_layer_forward_fp8": [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64,
                                       i64, i64, vp, vp, sz, vp],
             "moe_quantize_fp4_rows": [vp, i64, i64, vp, vp, vp],
+            "moe_rmsnorm": [vp, vp, vp, i64, i64, C.c_float, vp, vp, vp],
+            "moe_rmsnorm_fp8": [vp, vp, vp, i64, i64, C.c_float, vp, vp, vp, vp, vp],
+            "moe_rmsnorm_int8": [vp, vp, vp, i64, i64, C.c_float, vp, vp, vp, vp, vp],
+            "moe_rmsnorm_backward_workspace_size": [i64, i64, C.POINTER(sz)],
+            "moe_rmsnorm_backward": [vp, vp, vp, vp, i64, i64, C.c_float, vp, vp, vp, sz, vp],
+            "moe_quantize_int8_rows": [vp, i64, i64, vp, vp, vp],
+            "moe_gemm_int8": [vp, vp, vp, vp, i64, i64, i64, vp, vp, sz, vp],
+            "moe_grouped_gemm_int8": [vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, sz, vp],
+            "moe_permute_int8": [vp, vp, vp, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+            "moe_combine_weighted": [vp, vp, vp, vp, i64, i64, i64, vp, vp],
+            "moe_combine_weighted_backward": [vp, vp, vp, vp, i64, i64, i64, vp, vp, vp],
+            "moe_permute_backward": [vp, vp, vp, i64, i64, i64, vp, vp],
             "moe_layer_forward_fp4": [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64,
                                       i64, i64, vp, vp, sz, vp],
         }
@@ -409,3 +424,248 @@ def workspace_views_fp8(ws: torch.Tensor, T: int, d: int, f: int, E: int, k: int
         nbytes = n * torch.tensor([], dtype=dt).element_size()
         views[name] = ws[off:off + nbytes].view(dt).view(shape)
     return views
+
+
+# ---------------------------------------------------------------- norms, int8 products, sorted rows
+# These wrappers take tensors on the current device and refuse others; outputs
+# that the caller does not give are allocated for the stream the work runs on.
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise AssertionError(what)
+
+
+def _tensors(dtype, *named):
+    """Each (tensor, shape, name): contiguous, on the current device, of this dtype and shape."""
+    dev = torch.cuda.current_device()
+    for t, shape, name in named:
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+            raise AssertionError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, "
+                                 f"got {t.dtype} {tuple(t.shape)}, strides {tuple(t.stride())}, on {t.device}")
+
+
+def _rows_of(t: torch.Tensor, name: str):
+    _need(t.dim() == 2, f"{name}: expected 2 dimensions, got {t.dim()}")
+    return t.shape
+
+
+def _empty(stream, *specs, make=torch.empty):
+    """New tensors (shape, dtype) on the current device, owned by the stream that will write them."""
+    dev = torch.cuda.current_device()
+    if stream is None:
+        return [make(shape, dtype=dt, device=dev) for shape, dt in specs]
+    _need(stream.device_index == dev, f"stream: expected one of cuda:{dev}, got one of {stream.device}")
+    with torch.cuda.stream(stream):
+        return [make(shape, dtype=dt, device=dev) for shape, dt in specs]
+
+
+def _queue(stream) -> int:
+    """The handle of the stream the work goes to: the given one, or the current device's current stream."""
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    dev = torch.cuda.current_device()
+    _need(stream.device_index == dev, f"stream: expected one of cuda:{dev}, got one of {stream.device}")
+    return stream.cuda_stream
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _norm_args(x, weight, residual, xsum, y, stream):
+    T, d = _rows_of(x, "x")
+    rows = (T, d)
+    named = [(x, rows, "x"), (weight, (d,), "weight")]
+    if residual is not None:
+        named.append((residual, rows, "residual"))
+        if xsum is None:
+            (xsum,) = _empty(stream, (rows, torch.bfloat16))
+        else:
+            named.append((xsum, rows, "xsum"))
+    else:
+        _need(xsum is None, "xsum is the sum with a residual; there is none")
+    if y is not None:
+        named.append((y, rows, "y"))
+    _tensors(torch.bfloat16, *named)
+    return T, d, xsum
+
+
+def moe_rmsnorm(x, weight, eps: float, residual=None, xsum=None, y=None, stream=None):
+    """y = rmsnorm(x) * weight; with a residual, (rmsnorm(x + residual) * weight, x + residual)."""
+    T, d, xsum = _norm_args(x, weight, residual, xsum, y, stream)
+    if y is None:
+        (y,) = _empty(stream, ((T, d), torch.bfloat16))
+    _call("moe_rmsnorm", _ptr(x), _ptr(residual), _ptr(weight), T, d, eps, _ptr(xsum), _ptr(y), _queue(stream))
+    return y if residual is None else (y, xsum)
+
+
+def moe_rmsnorm_fp8(x, weight, eps: float, residual=None, xsum=None, y=None, stream=None):
+    """moe_rmsnorm with e4m3 codes and 1 x 128 scales: (q, scales) or, with a residual, (q, scales, xsum).
+    ``y`` (optional, given by the caller) also receives the bf16 result."""
+    T, d, xsum = _norm_args(x, weight, residual, xsum, y, stream)
+    q, sc = _empty(stream, ((T, d), torch.uint8), ((T, d // 128), torch.float32))
+    _call("moe_rmsnorm_fp8", _ptr(x), _ptr(residual), _ptr(weight), T, d, eps, _ptr(xsum), _ptr(y), _ptr(q), _ptr(sc),
+          _queue(stream))
+    return (q, sc) if residual is None else (q, sc, xsum)
+
+
+def moe_rmsnorm_int8(x, weight, eps: float, residual=None, xsum=None, y=None, stream=None):
+    """moe_rmsnorm with int8 codes and one scale a row: (q, scale) or, with a residual, (q, scale, xsum).
+    ``y`` (optional, given by the caller) also receives the bf16 result."""
+    T, d, xsum = _norm_args(x, weight, residual, xsum, y, stream)
+    q, sc = _empty(stream, ((T, d), torch.int8), ((T,), torch.float32))
+    _call("moe_rmsnorm_int8", _ptr(x), _ptr(residual), _ptr(weight), T, d, eps, _ptr(xsum), _ptr(y), _ptr(q), _ptr(sc),
+          _queue(stream))
+    return (q, sc) if residual is None else (q, sc, xsum)
+
+
+def moe_rmsnorm_backward_workspace_size(T: int, d: int) -> int:
+    n = C.c_size_t(0)
+    _call("moe_rmsnorm_backward_workspace_size", T, d, C.byref(n))
+    return int(n.value)
+
+
+def moe_rmsnorm_backward(dy, xsum, weight, eps: float, dxsum=None, dx=None, dweight=None, ws=None, stream=None):
+    """(dx, dweight) of moe_rmsnorm: dx [T,d] bf16 (of x and of residual alike), dweight [d] fp32.
+    ``dxsum``: the gradient that reaches the stream itself.  ``ws``: a uint8 tensor of
+    moe_rmsnorm_backward_workspace_size bytes, made here when not given."""
+    T, d = _rows_of(dy, "dy")
+    rows = (T, d)
+    named = [(dy, rows, "dy"), (xsum, rows, "xsum"), (weight, (d,), "weight")]
+    if dxsum is not None:
+        named.append((dxsum, rows, "dxsum"))
+    if dx is not None:
+        named.append((dx, rows, "dx"))
+    _tensors(torch.bfloat16, *named)
+    if dweight is not None:
+        _tensors(torch.float32, (dweight, (d,), "dweight"))
+    if ws is not None:
+        _tensors(torch.uint8, (ws, (ws.numel(),), "ws"))
+    if dx is None:
+        (dx,) = _empty(stream, (rows, torch.bfloat16))
+    if dweight is None:
+        (dweight,) = _empty(stream, ((d,), torch.float32))
+    if ws is None:
+        (ws,) = _empty(stream, ((moe_rmsnorm_backward_workspace_size(T, d),), torch.uint8))
+    _call("moe_rmsnorm_backward", _ptr(dy), _ptr(xsum), _ptr(weight), _ptr(dxsum), T, d, eps, _ptr(dx), _ptr(dweight),
+          _ptr(ws), ws.numel(), _queue(stream))
+    return dx, dweight
+
+
+def moe_quantize_int8_rows(x: torch.Tensor, stream=None):
+    """One scale a row: bf16 [R, C] (or [E, R, C], taken as [E*R, C]) -> (int8 codes, fp32 scales, one a row)."""
+    _need(x.dim() >= 2, "x: expected 2 dimensions or more")
+    _tensors(torch.bfloat16, (x, x.shape, "x"))
+    Cc = x.shape[-1]
+    R = x.numel() // Cc if Cc else 0
+    q, sc = _empty(stream, (x.shape, torch.int8), (x.shape[:-1], torch.float32))
+    _call("moe_quantize_int8_rows", _ptr(x), R, Cc, _ptr(q), _ptr(sc), _queue(stream))
+    return q, sc
+
+
+def moe_gemm_int8(xq, sx, Wq, sw, ws: torch.Tensor, out=None, stream=None):
+    """out [T,N] bf16 = (xq [T,K] Wq [N,K]^T) * sx [T] * sw [N]; ``ws``: any initialised workspace."""
+    (T, K), (N, _) = _rows_of(xq, "xq"), _rows_of(Wq, "Wq")
+    _tensors(torch.int8, (xq, (T, K), "xq"), (Wq, (N, K), "Wq"))
+    _tensors(torch.float32, (sx, (T,), "sx"), (sw, (N,), "sw"))
+    _tensors(torch.uint8, (ws, (ws.numel(),), "ws"))
+    if out is None:
+        (out,) = _empty(stream, ((T, N), torch.bfloat16))
+    else:
+        _tensors(torch.bfloat16, (out, (T, N), "out"))
+    _call("moe_gemm_int8", _ptr(xq), _ptr(sx), _ptr(Wq), _ptr(sw), T, K, N, _ptr(out), _ptr(ws), ws.numel(),
+          _queue(stream))
+    return out
+
+
+def moe_grouped_gemm_int8(xpq, sxp, counts, offsets, Wq, sw, T: int, k: int, ws: torch.Tensor, out=None, stream=None):
+    """out [T*k,N] bf16: the int8 product of expert e's matrix Wq[e] [N,K] for the rows of its segment.
+    Rows past offsets[E] are left as they are (unset in a new ``out``)."""
+    P, K = _rows_of(xpq, "xpq")
+    _need(Wq.dim() == 3, "Wq: expected [E, N, K]")
+    E, N, _ = Wq.shape
+    _need(P == T * k, f"xpq: expected {T} * {k} rows, got {P}")
+    _tensors(torch.int8, (xpq, (P, K), "xpq"), (Wq, (E, N, K), "Wq"))
+    _tensors(torch.float32, (sxp, (P,), "sxp"), (sw, (E, N), "sw"))
+    _tensors(torch.int32, (counts, (E,), "counts"), (offsets, (E + 1,), "offsets"))
+    _tensors(torch.uint8, (ws, (ws.numel(),), "ws"))
+    if out is None:
+        (out,) = _empty(stream, ((P, N), torch.bfloat16))
+    else:
+        _tensors(torch.bfloat16, (out, (P, N), "out"))
+    _call("moe_grouped_gemm_int8", _ptr(xpq), _ptr(sxp), _ptr(counts), _ptr(offsets), _ptr(Wq), _ptr(sw), T, K, N, E, k,
+          _ptr(out), _ptr(ws), ws.numel(), _queue(stream))
+    return out
+
+
+def moe_permute_int8(topk_idx, xq, sx, E: int, ws: torch.Tensor, stream=None):
+    """counts, offsets, perm, inv_perm, xpq, sxp: moe_permute of int8 rows xq [T,d] with scales sx [T].
+    Rows of xpq and sxp past offsets[E] are unset."""
+    (T, k), (_, d) = _rows_of(topk_idx, "topk_idx"), _rows_of(xq, "xq")
+    P = T * k
+    _tensors(torch.int32, (topk_idx, (T, k), "topk_idx"))
+    _tensors(torch.int8, (xq, (T, d), "xq"))
+    _tensors(torch.float32, (sx, (T,), "sx"))
+    _tensors(torch.uint8, (ws, (ws.numel(),), "ws"))
+    i32 = torch.int32
+    # an empty batch enqueues no work: its counts are set here
+    counts, offsets = _empty(stream, ((E,), i32), ((E + 1,), i32), make=torch.empty if T else torch.zeros)
+    perm, inv, xpq, sxp = _empty(stream, ((P,), i32), ((P,), i32), ((P, d), torch.int8), ((P,), torch.float32))
+    _call("moe_permute_int8", _ptr(topk_idx), _ptr(xq), _ptr(sx), T, d, E, k, _ptr(counts), _ptr(offsets), _ptr(perm),
+          _ptr(inv), _ptr(xpq), _ptr(sxp), _ptr(ws), ws.numel(), _queue(stream))
+    return counts, offsets, perm, inv, xpq, sxp
+
+
+def moe_combine_weighted(y_p, inv_perm, topk_w, shared_out=None, out=None, stream=None):
+    """out[t] = sum_j topk_w[t,j] y_p[inv_perm[t*k+j]] (+ shared_out[t]); T and k are topk_w's."""
+    (T, k), (P, d) = _rows_of(topk_w, "topk_w"), _rows_of(y_p, "y_p")
+    named = [(y_p, (T * k, d), "y_p")]
+    if shared_out is not None:
+        named.append((shared_out, (T, d), "shared_out"))
+    if out is not None:
+        named.append((out, (T, d), "out"))
+    _tensors(torch.bfloat16, *named)
+    _tensors(torch.float32, (topk_w, (T, k), "topk_w"))
+    _tensors(torch.int32, (inv_perm, (T * k,), "inv_perm"))
+    if out is None:
+        (out,) = _empty(stream, ((T, d), torch.bfloat16))
+    _call("moe_combine_weighted", _ptr(y_p), _ptr(inv_perm), _ptr(topk_w), _ptr(shared_out), T, k, d, _ptr(out),
+          _queue(stream))
+    return out
+
+
+def moe_combine_weighted_backward(dout, y_p, inv_perm, topk_w, dy_p=None, dw=None, stream=None):
+    """(dy_p [T*k,d] bf16, dw [T,k] fp32) of moe_combine_weighted; ``dy_p`` may be ``y_p``.
+    Rows of a new dy_p that no pair has (dropped pairs) are zero only if the caller gives them so."""
+    (T, k), (P, d) = _rows_of(topk_w, "topk_w"), _rows_of(y_p, "y_p")
+    named = [(dout, (T, d), "dout"), (y_p, (T * k, d), "y_p")]
+    if dy_p is not None:
+        named.append((dy_p, (T * k, d), "dy_p"))
+    _tensors(torch.bfloat16, *named)
+    _tensors(torch.float32, (topk_w, (T, k), "topk_w"))
+    _tensors(torch.int32, (inv_perm, (T * k,), "inv_perm"))
+    if dw is not None:
+        _tensors(torch.float32, (dw, (T, k), "dw"))
+    if dy_p is None:
+        (dy_p,) = _empty(stream, ((T * k, d), torch.bfloat16))
+    if dw is None:
+        (dw,) = _empty(stream, ((T, k), torch.float32))
+    _call("moe_combine_weighted_backward", _ptr(dout), _ptr(y_p), _ptr(inv_perm), _ptr(topk_w), T, k, d, _ptr(dy_p),
+          _ptr(dw), _queue(stream))
+    return dy_p, dw
+
+
+def moe_permute_backward(dxp, inv_perm, T: int, k: int, addend=None, dx=None, stream=None):
+    """dx [T,d] bf16 of moe_permute: dx[t] = sum_j dxp[inv_perm[t*k+j]] (+ addend[t])."""
+    P, d = _rows_of(dxp, "dxp")
+    named = [(dxp, (T * k, d), "dxp")]
+    if addend is not None:
+        named.append((addend, (T, d), "addend"))
+    if dx is not None:
+        named.append((dx, (T, d), "dx"))
+    _tensors(torch.bfloat16, *named)
+    _tensors(torch.int32, (inv_perm, (T * k,), "inv_perm"))
+    if dx is None:
+        (dx,) = _empty(stream, ((T, d), torch.bfloat16))
+    _call("moe_permute_backward", _ptr(dxp), _ptr(inv_perm), _ptr(addend), T, k, d, _ptr(dx), _queue(stream))
+    return dx

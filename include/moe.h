@@ -262,6 +262,109 @@ MOE_API int moe_layer_forward_fp4(const moe_bf16 *x, const moe_bf16 *Wg, const f
                                   int64_t T, int64_t d, int64_t f, int64_t E, int64_t k, moe_bf16 *out, void *ws,
                                   size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------- norms
+ * The residual's addition with a root-mean-square norm, the step before every
+ * layer:
+ *   s = bf16(x + residual)                       (residual NULL: s = x)
+ *   y = bf16( s / sqrt(mean(s^2) + eps) * weight )
+ * x, residual, s (xsum), y [T,d]; weight [d]; eps > 0.  Sums are fp32.  xsum is
+ * the stream to add the layer's output to; it is given exactly when residual
+ * is, and may be x or residual itself; y may be x.  Other overlaps are not
+ * allowed.  d is a multiple of 64 (128 for FP8), at most 32768. */
+MOE_API int moe_rmsnorm(const moe_bf16 *x, const moe_bf16 *residual, const moe_bf16 *weight, int64_t T, int64_t d,
+                        float eps, moe_bf16 *xsum, moe_bf16 *y, void *stream);
+
+/* The same with y in e4m3 codes and 1 x 128 scales: q [T,d], scales [T,d/128],
+ * bit-identical to moe_quantize_fp8_rows of moe_rmsnorm's y.  y may be NULL. */
+MOE_API int moe_rmsnorm_fp8(const moe_bf16 *x, const moe_bf16 *residual, const moe_bf16 *weight, int64_t T, int64_t d,
+                            float eps, moe_bf16 *xsum, moe_bf16 *y, uint8_t *q, float *scales, void *stream);
+
+/* The same with y in int8 codes and one scale a row: q [T,d], scale [T],
+ * bit-identical to moe_quantize_int8_rows of moe_rmsnorm's y.  y may be NULL. */
+MOE_API int moe_rmsnorm_int8(const moe_bf16 *x, const moe_bf16 *residual, const moe_bf16 *weight, int64_t T, int64_t d,
+                             float eps, moe_bf16 *xsum, moe_bf16 *y, int8_t *q, float *scale, void *stream);
+
+/* Workspace bytes of moe_rmsnorm_backward for these sizes (0 at T = 0). */
+MOE_API int moe_rmsnorm_backward_workspace_size(int64_t T, int64_t d, size_t *bytes);
+
+/* The gradient of moe_rmsnorm.  With xsum = s, rstd = 1 / sqrt(mean(s^2) + eps),
+ * n = s rstd and g = dy * weight:
+ *   dx      = bf16( (g - n mean(g n)) rstd + dxsum )   [T,d]
+ *   dweight = sum over rows of dy * n                  [d], fp32
+ * dxsum [T,d] is the gradient that reaches the stream itself (NULL: none); dx is
+ * the gradient of x and of residual alike, and may be dy or dxsum itself.  The
+ * rows of dweight's sum are added in a fixed order (the same bits in every
+ * run).  T = 0 sets dweight to zero.  `ws` is scratch and needs no
+ * initialisation; two calls that may overlap need two. */
+MOE_API int moe_rmsnorm_backward(const moe_bf16 *dy, const moe_bf16 *xsum, const moe_bf16 *weight,
+                                 const moe_bf16 *dxsum, int64_t T, int64_t d, float eps, moe_bf16 *dx, float *dweight,
+                                 void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------- int8 products
+ * 8-bit integer codes with one scale a row (a token, or a channel of a weight
+ * matrix): scale = max|v| / 127, code = v * (127 / max|v|) rounded to nearest,
+ * ties to even, in -127..127.  A row whose largest magnitude is below 2^-100
+ * counts as zero (scale 1).  A row that holds a NaN or an infinity gets the
+ * scale NaN, so every product of it is NaN. */
+
+/* x [rows, cols] bf16 -> q [rows, cols], scale [rows].  cols a multiple of 64,
+ * at most 32768.  Expert weights are quantised as one matrix, [E*N, K]. */
+MOE_API int moe_quantize_int8_rows(const moe_bf16 *x, int64_t rows, int64_t cols, int8_t *q, float *scale,
+                                   void *stream);
+
+/* out [T,N] = bf16( (xq Wq^T)[t,n] * sx[t] * sw[n] ): xq [T,K], sx [T], Wq [N,K],
+ * sw [N].  The integer sum is exact (codes -128..127); it is converted to fp32
+ * and scaled there.  K and N multiples of 64, K at most 65536.  `ws` (at least
+ * 256 bytes, initialised like every workspace) supplies the device error word
+ * and holds nothing else of this call. */
+MOE_API int moe_gemm_int8(const int8_t *xq, const float *sx, const int8_t *Wq, const float *sw, int64_t T, int64_t K,
+                          int64_t N, moe_bf16 *out, void *ws, size_t ws_bytes, void *stream);
+
+/* The same with one matrix an expert, on rows sorted by expert: for every expert
+ * e and row r in [offsets[e], offsets[e+1]), out[r,n] = bf16( (xpq[r] . Wq[e,n])
+ * * sxp[r] * sw[e,n] ).  xpq [T*k,K], sxp [T*k], counts [E] and offsets [E+1] as
+ * moe_permute_int8 leaves them, Wq [E,N,K], sw [E,N], out [T*k,N]; E*N < 2^31.
+ * Rows past offsets[E] are left untouched.  The tile plan is built in `ws` (the
+ * control part of any workspace of these T, E, k), which two calls that may
+ * overlap must not share.  Segments outside the T*k rows set
+ * MOE_DEVERR_PLAN and nothing is computed. */
+MOE_API int moe_grouped_gemm_int8(const int8_t *xpq, const float *sxp, const int32_t *counts, const int32_t *offsets,
+                                  const int8_t *Wq, const float *sw, int64_t T, int64_t K, int64_t N, int64_t E,
+                                  int64_t k, moe_bf16 *out, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------- sorted rows and their gradient */
+
+/* moe_permute for int8 rows with a scale each: xq [T,d], sx [T] -> xpq [T*k,d],
+ * sxp [T*k]; the other outputs, their order and the treatment of bad expert ids
+ * are moe_permute's.  Needs the control part of a workspace of these T, E, k. */
+MOE_API int moe_permute_int8(const int32_t *topk_idx, const int8_t *xq, const float *sx, int64_t T, int64_t d,
+                             int64_t E, int64_t k, int32_t *counts, int32_t *offsets, int32_t *perm,
+                             int32_t *inv_perm, int8_t *xpq, float *sxp, void *ws, size_t ws_bytes, void *stream);
+
+/* Rows back in token order with the gates applied (for expert outputs without
+ * them; moe_grouped_gemm's y_p carries them already and goes to moe_combine):
+ *   out[t,:] = bf16( sum_j topk_w[t,j] y_p[inv_perm[t*k+j], :] (+ shared_out[t,:]) )
+ * in fp32, ascending j, no atomics.  inv_perm is moe_permute's (every position
+ * at most once); a pair whose position lies outside [0, T*k) adds nothing. */
+MOE_API int moe_combine_weighted(const moe_bf16 *y_p, const int32_t *inv_perm, const float *topk_w,
+                                 const moe_bf16 *shared_out, int64_t T, int64_t k, int64_t d, moe_bf16 *out,
+                                 void *stream);
+
+/* Its gradient: dy_p[inv_perm[t*k+j], :] = bf16( topk_w[t,j] dout[t,:] ) and
+ * dw[t,j] = <dout[t,:], y_p[inv_perm[t*k+j], :]> (fp32, [T,k]).  A pair without
+ * a position gets dw = 0; rows of dy_p that no pair has are left untouched.
+ * The gradient of shared_out is dout itself.  dy_p may be y_p. */
+MOE_API int moe_combine_weighted_backward(const moe_bf16 *dout, const moe_bf16 *y_p, const int32_t *inv_perm,
+                                          const float *topk_w, int64_t T, int64_t k, int64_t d, moe_bf16 *dy_p,
+                                          float *dw, void *stream);
+
+/* The gradient of moe_permute's row gather: dx[t,:] = bf16( sum_j
+ * dxp[inv_perm[t*k+j], :] (+ addend[t,:]) ), in fp32, ascending j.  addend [T,d]
+ * (NULL: none) is a gradient that reaches x on another way, such as the
+ * router's; it may be dx itself. */
+MOE_API int moe_permute_backward(const moe_bf16 *dxp, const int32_t *inv_perm, const moe_bf16 *addend, int64_t T,
+                                 int64_t k, int64_t d, moe_bf16 *dx, void *stream);
+
 /* Per-phase timing of the next moe_layer_forward call made on this host
  * thread: `events` holds n >= 6 cudaEvent_t handles; that call records
  * events[0..5] on its stream before the router, the permutation, the gate/up
