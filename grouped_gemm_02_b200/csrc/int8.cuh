@@ -22,24 +22,27 @@
 //              with fewer tiles than SMs, bound by the weights' bytes.  The sums
 //              are integers, so the split changes no bit.
 //
-// Warp roles as in grouped_gemm.cuh: warp 0 TMA producer, warp 1 MMA issuer,
-// warps 2-5 epilogue; two TMEM accumulators of 256 columns; every wait is
-// bounded.  All loads come after griddepcontrol.wait: weights may be the output
+// Warp roles: warp 0 TMA producer, warp 1 MMA issuer, warps 2-9 epilogue (two a
+// TMEM lane quadrant, every other 16 columns each); two TMEM accumulators of 256
+// columns; every wait is bounded.  All loads come after griddepcontrol.wait: weights may be the output
 // of the kernel before (a quantiser).
 #pragma once
 
 #include "common.cuh"
 #include "grouped_gemm.cuh"
+#include "int8_shape.h"
 #include "ptx.cuh"
 
 namespace moe {
 
-constexpr int I8_SINGLE = 0, I8_PAIR = 1, I8_SPLIT = 2;
-constexpr int kI8BlockK = 128;                   // codes per K block
 constexpr int kI8MaxK = 1 << 16;
+constexpr int kI8Epilogues = 8;                  // epilogue warps
+constexpr int kI8Threads = 64 + 32 * kI8Epilogues;
 constexpr int kI8RingBytes = 200 * 1024;
-constexpr int kI8SmemBytes = 1024 + kI8RingBytes + kBarBytes + (int)sizeof(SmemPlan);
+constexpr int kI8ScaleBytes = kI8Epilogues * 256 * 4;       // each epilogue warp's copy of its tile's row scales
+constexpr int kI8SmemBytes = 1024 + kI8RingBytes + kBarBytes + (int)sizeof(SmemPlan) + kI8ScaleBytes;
 static_assert(kI8SmemBytes <= 227 * 1024, "shared memory budget");
+static_assert(sizeof(SmemPlan) % 16 == 0 && kBarBytes % 16 == 0, "the scales are read as float4");
 static_assert(128 * 256 * 4 <= kI8RingBytes, "the int32 tile of I8_SPLIT reuses the ring");
 
 struct Int8Args {
@@ -102,8 +105,38 @@ __device__ __forceinline__ I8Tile i8_tile(int t, int nb, const Int8Args& a, cons
     return tl;
 }
 
+// 16 columns of one warp's accumulator quadrant, lane = channel, as bf16 pairs of
+// neighbouring columns (w[p] holds columns 2p and 2p + 1 of this lane's channel),
+// turned so that each lane holds 8 consecutive channels of a column: on return
+// o[r] is channels 8 (lane / 8) .. + 7 of column 8 r + lane % 8.  Three rounds of
+// exchange between lanes that differ in bit 0, 1 and 2: 16 shuffles for 16
+// columns, and the global store is then 16 bytes a lane instead of 2.
+__device__ __forceinline__ void i8_turn16(const uint32_t (&w)[8], uint4 (&o)[2], int lane)
+{
+    const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
+    uint32_t a[8];      // column 2p + b0: channels 2 (lane / 2), + 1
+#pragma unroll
+    for (int p = 0; p < 8; p++) {
+        const uint32_t r = __shfl_xor_sync(0xffffffffu, w[p], 1);
+        a[p] = b0 ? __byte_perm(r, w[p], 0x7632) : __byte_perm(w[p], r, 0x5410);
+    }
+    uint32_t b[4][2];   // column 4q + 2 b1 + b0: channels 4 (lane / 4) .. + 3
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+        const uint32_t r = __shfl_xor_sync(0xffffffffu, b1 ? a[2 * q] : a[2 * q + 1], 2);
+        b[q][0] = b1 ? r : a[2 * q];
+        b[q][1] = b1 ? a[2 * q + 1] : r;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const uint32_t r0 = __shfl_xor_sync(0xffffffffu, b2 ? b[2 * h][0] : b[2 * h + 1][0], 4);
+        const uint32_t r1 = __shfl_xor_sync(0xffffffffu, b2 ? b[2 * h][1] : b[2 * h + 1][1], 4);
+        o[h] = b2 ? make_uint4(r0, r1, b[2 * h + 1][0], b[2 * h + 1][1]) : make_uint4(b[2 * h][0], b[2 * h][1], r0, r1);
+    }
+}
+
 template <int FORM>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(kI8Threads, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB16,
                      const __grid_constant__ CUtensorMap mB64, const Int8Args a)
 {
@@ -161,7 +194,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         for (int i = 0; i < 2; i++) {
             ptx::mbar_init(ptx::smem_u32(&ctl->tfull[i]), 1);
-            ptx::mbar_init(ptx::smem_u32(&ctl->tempty[i]), PAIR ? 8 : 4);
+            ptx::mbar_init(ptx::smem_u32(&ctl->tempty[i]), PAIR ? 2 * kI8Epilogues : kI8Epilogues);
         }
         ptx::mbar_init(ptx::smem_u32(&ctl->drain), 1);
         ctl->abort = 0;
@@ -296,26 +329,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             }
         }
     } else {
-        // ------------------------------------------------------------ epilogue (warps 2-5)
-        const int quad = warp & 3;
+        // ------------------------------------------------------------ epilogue (warps 2-9)
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        float* s_sx = reinterpret_cast<float*>(smem + kI8RingBytes + kBarBytes + sizeof(SmemPlan)) + (warp - 2) * 256;
         int acc = 0;
         uint32_t aph = 0;
         for (int t = first; t < total; t += step) {
             const I8Tile tl = i8_tile<FORM>(t, nb, a, splan, rank);
-            // scales, fetched before the accumulator wait: a channel a lane, rows l + 32 i of lane l
-            const int ch = tl.ma * 128 + quad * 32 + lane;
+            // scales, fetched before the accumulator wait: a channel a lane, the tile's rows in shared memory
+            const int ch0 = tl.ma * 128 + quad * 32, ch = ch0 + lane;
             const float sw = (FORM != I8_SPLIT && ch < a.N) ? __ldg(a.sw + (size_t)tl.e * a.N + ch) : 0.f;
-            float sx[8];
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const int col = 32 * i + lane;
-                sx[i] = (FORM != I8_SPLIT && col < tl.rows) ? __ldg(a.sx + tl.row0 + col) : 0.f;
+            if (FORM != I8_SPLIT) {
+                __syncwarp();       // the last tile's scales have been read
+                for (int i = lane; i < tl.n_mma; i += 32) {
+                    const int col = 2 * (i & ~15) + 16 * half + (i & 15);   // the columns this warp takes
+                    if (col >= tl.n_mma) break;
+                    s_sx[col] = col < tl.rows ? __ldg(a.sx + tl.row0 + col) : 0.f;
+                }
+                __syncwarp();
             }
             const bool ok = bounded_wait(ptx::smem_u32(&ctl->tfull[acc]), aph, ctl, a.err);
             if (!__all_sync(0xffffffffu, ok)) break;
             ptx::tc_fence_after();
             const uint32_t taddr = tmem_base + (uint32_t)acc * 256u + ((uint32_t)(quad * 32) << 16);
-            for (int c0 = 0; c0 < tl.n_mma; c0 += 16) {
+            for (int c0 = 16 * half; c0 < tl.n_mma; c0 += 32) {
                 uint32_t v[16];
                 ptx::tmem_ld16(taddr + (uint32_t)c0, v);
                 ptx::tmem_ld_wait();
@@ -327,16 +364,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     for (int j = 0; j < 16; j++)
                         red[(c0 + j) * 128 + quad * 32 + lane] = (int)v[j];
                 } else {
-                    const int gi = c0 >> 5;
-                    const float mine = gi == 0 ? sx[0] : gi == 1 ? sx[1] : gi == 2 ? sx[2] : gi == 3 ? sx[3]
-                                     : gi == 4 ? sx[4] : gi == 5 ? sx[5] : gi == 6 ? sx[6] : sx[7];
+                    uint32_t w[8];
 #pragma unroll
-                    for (int j = 0; j < 16; j++) {
-                        const float sc = __shfl_sync(0xffffffffu, mine, (c0 & 31) + j);
-                        const int col = c0 + j;
-                        if (col < tl.rows && ch < a.N)
-                            a.out[(size_t)(tl.row0 + col) * a.N + ch] =
-                                __float2bfloat16_rn((float)(int)v[j] * sc * sw);
+                    for (int j = 0; j < 4; j++) {
+                        const float4 sc = reinterpret_cast<const float4*>(s_sx + c0)[j];
+                        const __nv_bfloat162 lo = __floats2bfloat162_rn((float)(int)v[4 * j] * sc.x * sw,
+                                                                        (float)(int)v[4 * j + 1] * sc.y * sw);
+                        const __nv_bfloat162 hi = __floats2bfloat162_rn((float)(int)v[4 * j + 2] * sc.z * sw,
+                                                                        (float)(int)v[4 * j + 3] * sc.w * sw);
+                        w[2 * j] = *reinterpret_cast<const uint32_t*>(&lo);
+                        w[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+                    }
+                    uint4 o[2];
+                    i8_turn16(w, o, lane);
+                    const int oc = ch0 + (lane >> 3) * 8;
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const int col = c0 + 8 * h + (lane & 7);
+                        if (col < tl.rows && oc < a.N)   // N % 8 == 0: all 8 channels or none
+                            *reinterpret_cast<uint4*>(a.out + (size_t)(tl.row0 + col) * a.N + oc) = o[h];
                     }
                 }
             }
@@ -360,7 +406,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (first < total) {
             const I8Tile tl = i8_tile<FORM>(first, nb, a, splan, rank);
             const int items = tl.rows * 32;
-            for (int i = rank * kGemmThreads + (int)threadIdx.x; i < items; i += split * kGemmThreads) {
+            for (int i = rank * kI8Threads + (int)threadIdx.x; i < items; i += split * kI8Threads) {
                 const int col = i >> 5, c4 = (i & 31) * 4;
                 const int ch = tl.ma * 128 + c4;
                 if (ch >= a.N) continue;       // N % 4 == 0: all four channels or none

@@ -204,7 +204,7 @@ int device_setup(DeviceState** out)
             pc8 = std::min(pc8, max_pair_clusters(grouped_gemm_fp8_kernel<FP8_DOWN, true, true>, kFp8SmemBytes,
                                                   kFp8Threads));
             st.fp8_pair_grid = 2 * std::min(pc8, sms / 2);
-            st.i8_pair_grid = 2 * std::min(max_pair_clusters(int8_gemm_kernel<I8_PAIR>, kI8SmemBytes), sms / 2);
+            st.i8_pair_grid = 2 * std::min(max_pair_clusters(int8_gemm_kernel<I8_PAIR>, kI8SmemBytes, kI8Threads), sms / 2);
             if (!g_encode) {
                 cudaDriverEntryPointQueryResult q;
                 void* fn = nullptr;
@@ -1431,6 +1431,26 @@ int norm_entry(const moe_bf16* x, const moe_bf16* residual, const moe_bf16* weig
 constexpr PlanShape kPlanI8{kTileRows, 64, 128, 16, 0, kTilesCap};
 constexpr PlanShape kPlanI8Pair{kTileRows, 128, 256, 32, 1, kTilesCap};
 
+// Launches a product in one of its forms; `split` CTAs share a tile in I8_SPLIT.
+int run_int8(const Int8Args& a, const void* xq, int64_t rows, const void* Wq, int64_t wrows, int form, int64_t tiles,
+             int split, const DeviceState* dev, cudaStream_t st)
+{
+    CUtensorMap ma, mb16, mb64;
+    if (!make_map_u8(&ma, Wq, a.K, wrows, 128) || !make_map_u8(&mb16, xq, a.K, rows, 16) ||
+        !make_map_u8(&mb64, xq, a.K, rows, 64))
+        return MOE_ERR_CUDA;
+    const dim3 block(kI8Threads);
+    if (form == I8_PAIR)
+        return status_of(launch_cluster(int8_gemm_kernel<I8_PAIR>, 2,
+                                        dim3((unsigned)std::min<int64_t>(2 * tiles, dev->i8_pair_grid)), block,
+                                        kI8SmemBytes, st, ma, mb16, mb64, a));
+    if (form == I8_SPLIT)
+        return status_of(launch_cluster(int8_gemm_kernel<I8_SPLIT>, split, dim3((unsigned)tiles * split), block,
+                                        kI8SmemBytes, st, ma, mb16, mb64, a));
+    return status_of(launch(int8_gemm_kernel<I8_SINGLE>, dim3((unsigned)std::min<int64_t>(tiles, dev->sm_count)),
+                            block, kI8SmemBytes, st, ma, mb16, mb64, a));
+}
+
 int check_int8(int64_t N, int64_t K)
 {
     if (N <= 0 || K <= 0 || N >= (int64_t(1) << 31) || K > kI8MaxK) return MOE_ERR_ARG;
@@ -1538,24 +1558,20 @@ int moe_gemm_int8(const int8_t* xq, const float* sx, const int8_t* Wq, const flo
     if (ws_bytes < 256) return MOE_ERR_WS;   // the error word
     DeviceState* dev;
     if ((rc = device_setup(&dev))) return rc;
-    cudaStream_t st = as_stream(stream);
-    CUtensorMap ma, mb16, mb64;
-    if (!make_map_u8(&ma, Wq, K, N, 128) || !make_map_u8(&mb16, xq, K, T, 16) || !make_map_u8(&mb64, xq, K, T, 64))
-        return MOE_ERR_CUDA;
     Int8Args a{};
     a.T = (int)T;
-    a.units = (int)((T + kTileRows - 1) / kTileRows);
-    a.chunk = (int)((T + a.units - 1) / a.units + 15) / 16 * 16;
     a.N = (int)N;
     a.K = (int)K;
     a.sx = sx;
     a.sw = sw;
     a.out = reinterpret_cast<bf16*>(out);
     a.err = static_cast<uint32_t*>(ws);
-    const int64_t tiles = (N + 127) / 128 * a.units;
-    if (tiles >= (int64_t(1) << 31)) return MOE_ERR_ARG;
-    return status_of(launch(int8_gemm_kernel<I8_SINGLE>, dim3((unsigned)std::min<int64_t>(tiles, dev->sm_count)),
-                            dim3(kGemmThreads), kI8SmemBytes, st, ma, mb16, mb64, a));
+    const Int8Shape sh = i8_shape(T, K, N, dev->sm_count, dev->i8_pair_grid >= 2,
+                                  policy(g_policy_pair, "MOE_GEMM_PAIR", /*invert=*/false));
+    if (sh.units == 0) return MOE_ERR_ARG;   // more tiles than a launch can count
+    a.chunk = sh.chunk;
+    a.units = sh.units;
+    return run_int8(a, xq, T, Wq, N, sh.form, sh.tiles, sh.split, dev, as_stream(stream));
 }
 
 int moe_grouped_gemm_int8(const int8_t* xpq, const float* sxp, const int32_t* counts, const int32_t* offsets,
@@ -1576,12 +1592,11 @@ int moe_grouped_gemm_int8(const int8_t* xpq, const float* sxp, const int32_t* co
     cudaStream_t st = as_stream(stream);
     int32_t* plan = at<int32_t>(ws, L.plan);
     const int64_t P = T * k;
-    const PlanShape ps = kPlanI8;
+    const int forced = policy(g_policy_pair, "MOE_GEMM_PAIR", /*invert=*/false);
+    const bool pair = dev->i8_pair_grid >= 2 && (forced >= 0 ? forced == 1 : P >= 256);
+    const PlanShape ps = pair ? kPlanI8Pair : kPlanI8;
     if (launch(plan_kernel, dim3(1), dim3(1024), 0, st, counts, offsets, (int)E, plan, 0, (int)N, 0, 0, ps) !=
         cudaSuccess)
-        return MOE_ERR_CUDA;
-    CUtensorMap ma, mb16, mb64;
-    if (!make_map_u8(&ma, Wq, K, E * N, 128) || !make_map_u8(&mb16, xpq, K, P, 16) || !make_map_u8(&mb64, xpq, K, P, 64))
         return MOE_ERR_CUDA;
     Int8Args a{};
     a.plan = plan;
@@ -1592,8 +1607,7 @@ int moe_grouped_gemm_int8(const int8_t* xpq, const float* sxp, const int32_t* co
     a.sw = sw;
     a.out = reinterpret_cast<bf16*>(out);
     a.err = at<uint32_t>(ws, L.err);
-    return status_of(launch(int8_gemm_kernel<I8_SINGLE>, dim3(dev->sm_count), dim3(kGemmThreads), kI8SmemBytes, st,
-                            ma, mb16, mb64, a));
+    return run_int8(a, xpq, P, Wq, E * N, pair ? I8_PAIR : I8_SINGLE, dev->sm_count, 1, dev, st);
 }
 
 int moe_permute_int8(const int32_t* topk_idx, const int8_t* xq, const float* sx, int64_t T, int64_t d, int64_t E,
