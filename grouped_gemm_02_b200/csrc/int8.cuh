@@ -40,13 +40,26 @@ constexpr int kI8Epilogues = 8;                  // epilogue warps
 constexpr int kI8Threads = 64 + 32 * kI8Epilogues;
 constexpr int kI8RingBytes = 200 * 1024;
 constexpr int kI8ScaleBytes = kI8Epilogues * 256 * 4;       // each epilogue warp's copy of its tile's row scales
-constexpr int kI8SmemBytes = 1024 + kI8RingBytes + kBarBytes + (int)sizeof(SmemPlan) + kI8ScaleBytes;
+
+// The tiles of a grouped product, built by every CTA for itself from counts and
+// offsets: one block for each expert with rows, heaviest first, cut into `units`
+// tiles of `chunk` rows.
+struct I8Plan {
+    int4 blk[kMaxExperts];          // expert, first row, rows, chunk
+    int n[kMaxExperts];             // rows by expert (zeros up to a multiple of 4: the ranking reads int4)
+    int units[kMaxExperts];
+    int tb[kMaxExperts + 1];        // prefix of units
+    int nb, widest, cap;
+};
+constexpr int kI8SmemBytes = 1024 + kI8RingBytes + kBarBytes + (int)sizeof(I8Plan) + kI8ScaleBytes;
 static_assert(kI8SmemBytes <= 227 * 1024, "shared memory budget");
-static_assert(sizeof(SmemPlan) % 16 == 0 && kBarBytes % 16 == 0, "the scales are read as float4");
+static_assert(sizeof(I8Plan) % 16 == 0 && kBarBytes % 16 == 0, "the scales are read as float4");
 static_assert(128 * 256 * 4 <= kI8RingBytes, "the int32 tile of I8_SPLIT reuses the ring");
 
 struct Int8Args {
-    const int32_t* plan;    // grouped: the tile plan; dense: null
+    const int32_t* counts;  // grouped: rows of each expert, and where they begin; dense: null
+    const int32_t* offsets;
+    int E;
     int T;                  // rows; dense: cut into `units` chunks of `chunk` rows
     int units, chunk;
     int N, K;
@@ -62,13 +75,13 @@ struct I8Tile {
 
 // Tile t of the launch.  rank: this CTA's place in its pair.
 template <int FORM>
-__device__ __forceinline__ I8Tile i8_tile(int t, int nb, const Int8Args& a, const SmemPlan* sp, int rank)
+__device__ __forceinline__ I8Tile i8_tile(int t, const Int8Args& a, const I8Plan* sp, int rank)
 {
     constexpr int kRows = FORM == I8_PAIR ? 256 : 128;
     I8Tile tl;
     int start, row_base, n;
     const int mt = (a.N + kRows - 1) / kRows;
-    if (!a.plan) {
+    if (!a.counts) {
         const int u = t / mt;
         tl.m = t - u * mt;
         tl.e = 0;
@@ -76,13 +89,17 @@ __device__ __forceinline__ I8Tile i8_tile(int t, int nb, const Int8Args& a, cons
         row_base = 0;
         n = min(a.chunk, a.T - start);
     } else {
-        int lo = 0, hi = nb - 1;
+        // tile t of block lo: channel block m of the unit's rows; the units of one channel
+        // block run together and share its weights in L2
+        int lo = 0, hi = sp->nb - 1;
+        const int tu = t / mt;     // prefix entries count units
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (sp->tb[mid] <= t) lo = mid;
+            if (sp->tb[mid] <= tu) lo = mid;
             else hi = mid - 1;
         }
-        const int local = t - sp->tb[lo], units = sp->units[lo];
+        const int units = sp->units[lo];
+        const int local = t - sp->tb[lo] * mt;
         const int4 b = sp->blk[lo];
         tl.e = b.x;
         tl.m = local / units;
@@ -103,6 +120,102 @@ __device__ __forceinline__ I8Tile i8_tile(int t, int nb, const Int8Args& a, cons
         tl.b_row0 = tl.row0;
     }
     return tl;
+}
+
+// Builds the plan of a grouped product (every thread of the CTA).  Returns false
+// when a segment lies outside the rows.  slots: CTAs (or pairs) of the launch.
+//
+// The rows of a tile: at most `cap`, the one of 256, 128, 64 and 32 that costs
+// the least by the terms of i8_cost (waves of tiles, each by its bytes at an
+// SM's share of L2): few, wide segments take narrower tiles until the SMs are
+// busy.  A block of n rows is cut into ceil(n / cap) units of equal width.
+__device__ __forceinline__ bool i8_plan(const Int8Args& a, I8Plan* p, int mt, int nk, int slots, bool pair)
+{
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int align = pair ? 32 : 16;
+    bool bad = false;
+    for (int e = tid; e < a.E; e += kI8Threads) {
+        const int n = a.counts[e], o = a.offsets[e];
+        bad |= n < 0 || n > a.T || (n > 0 && (o < 0 || o > a.T - n));
+        p->n[e] = n;
+    }
+    if (tid < ((-a.E) & 3)) p->n[a.E + tid] = 0;
+    if (__syncthreads_or(bad)) return false;
+    if (tid < 32) {
+        // total units under each cap, and the widest segment
+        int u[4] = {0, 0, 0, 0}, most = 0, nb = 0;
+        for (int e = lane; e < a.E; e += 32) {
+            const int n = p->n[e];
+#pragma unroll
+            for (int i = 0; i < 4; i++) u[i] += (n + (256 >> i) - 1) / (256 >> i);
+            most = max(most, n);
+            nb += n > 0;
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        float least = 0.f;
+        int cap = 256;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int units = __reduce_add_sync(0xffffffffu, u[i]);
+            const int w = min(256 >> i, max(most, 1));
+            const float waves = (float)(((int64_t)units * mt + slots - 1) / slots);
+            const float kb = fmaxf((128.f + (pair ? 0.5f : 1.f) * (float)w) * (128.f / 90.f), 1.5f * (float)w);
+            const float cost = waves * ((float)nk * kb + 170.f + 15.f * (float)w);
+            if (i == 0 || cost < least) {
+                least = cost;
+                cap = 256 >> i;
+            }
+        }
+        nb = __reduce_add_sync(0xffffffffu, nb);
+        if (lane == 0) {
+            p->cap = cap;
+            p->nb = nb;
+        }
+    }
+    __syncthreads();
+    const int cap = p->cap;
+    for (int e = tid; e < a.E; e += kI8Threads) {
+        const int n = p->n[e];
+        if (n == 0) continue;
+        int r = 0;      // rank: more rows first, then the lower expert
+#pragma unroll 4
+        for (int j = 0; j < a.E; j += 4) {
+            const int4 m = *reinterpret_cast<const int4*>(p->n + j);
+            r += m.x > n || (m.x == n && j < e);
+            r += m.y > n || (m.y == n && j + 1 < e);
+            r += m.z > n || (m.z == n && j + 2 < e);
+            r += m.w > n || (m.w == n && j + 3 < e);
+        }
+        const int units = (n + cap - 1) / cap;
+        const int chunk = ((n + units - 1) / units + align - 1) / align * align;
+        p->blk[r] = make_int4(e, a.offsets[e], n, chunk);
+        p->units[r] = units;
+    }
+    __syncthreads();
+    if (tid < 32) {
+        // prefix of units over the blocks, 32 at a time
+        const int nb = p->nb;
+        int run = 0, widest = 0;
+        for (int i = 0; i < nb; i += 32) {
+            const bool in = i + lane < nb;
+            int v = in ? p->units[i + lane] : 0;
+            if (in) widest = max(widest, p->blk[i + lane].w);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += x;
+            }
+            if (in) p->tb[i + lane + 1] = run + v;
+            run += __shfl_sync(0xffffffffu, v, 31);
+        }
+        widest = __reduce_max_sync(0xffffffffu, widest);
+        if (lane == 0) {
+            p->tb[0] = 0;
+            p->widest = max(widest, align);
+        }
+    }
+    __syncthreads();
+    return true;
 }
 
 // 16 columns of one warp's accumulator quadrant, lane = channel, as bf16 pairs of
@@ -144,7 +257,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     SmemCtl* ctl = reinterpret_cast<SmemCtl*>(smem + kI8RingBytes);
-    SmemPlan* splan = reinterpret_cast<SmemPlan*>(smem + kI8RingBytes + kBarBytes);
+    I8Plan* splan = reinterpret_cast<I8Plan*>(smem + kI8RingBytes + kBarBytes);
     const uint32_t ring = ptx::smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = FORM != I8_SINGLE ? (int)ptx::cluster_ctarank() : 0;
@@ -155,38 +268,26 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    const PlanHeader* hdr = reinterpret_cast<const PlanHeader*>(a.plan);
-    const int nb = a.plan ? hdr->n_blocks : 0;
     constexpr int kRows = PAIR ? 256 : 128;
-    const int total = a.plan ? hdr->tiles2 : a.units * ((a.N + kRows - 1) / kRows);
-    const int widest = a.plan ? hdr->n_max : min(a.chunk, a.T);
+    const int mt = (a.N + kRows - 1) / kRows;
+    const int nk = (a.K + kI8BlockK - 1) / kI8BlockK;
+    int total = a.units * mt, widest = min(a.chunk, a.T);
+    if (a.counts) {
+        if (!i8_plan(a, splan, mt, nk, step, PAIR)) {
+            // segments outside the rows: every CTA sees the same counts and leaves here
+            if (threadIdx.x == 0) atomicOr(a.err, DEVERR_PLAN);
+            return;
+        }
+        total = splan->tb[splan->nb] * mt;
+        widest = splan->widest;
+    }
     const int n_max = PAIR ? max(32, (widest + 31) & ~31) : max(16, (widest + 15) & ~15);
     const uint32_t stage_bytes = kATileBytes + (uint32_t)(PAIR ? n_max / 2 : n_max) * kBRowBytes;
     const int stages = min(kMaxStages, (int)(kI8RingBytes / stage_bytes));
-    const int nk = (a.K + kI8BlockK - 1) / kI8BlockK;
     // I8_SPLIT: this CTA's K blocks (the host launches no more CTAs a tile than K blocks)
     const int kb0 = FORM == I8_SPLIT ? (int)((int64_t)nk * rank / split) : 0;
     const int kb1 = FORM == I8_SPLIT ? (int)((int64_t)nk * (rank + 1) / split) : nk;
 
-    if (a.plan) {
-        const PlanArrays pa = plan_arrays(const_cast<int32_t*>(a.plan));
-        // counts and offsets are the caller's: segments outside the rows, or a plan cut
-        // for the other form, are refused by every CTA alike before any barrier
-        bool bad = hdr->pair != (PAIR ? 1 : 0);
-        for (int i = threadIdx.x; i <= nb; i += blockDim.x) {
-            splan->tb[i] = pa.tb2[i];
-            if (i < nb) {
-                const int4 b = make_int4(pa.group[i], pa.row0[i], pa.rows[i], pa.chunk[i]);
-                bad |= b.y < 0 || b.z <= 0 || b.z > a.T || b.y > a.T - b.z;
-                splan->blk[i] = b;
-                splan->units[i] = pa.units[i];
-            }
-        }
-        if (__syncthreads_or(bad)) {
-            if (threadIdx.x == 0) atomicOr(a.err, DEVERR_PLAN);
-            return;
-        }
-    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; s++) {
             ptx::mbar_init(ptx::smem_u32(&ctl->full[s]), 1);
@@ -233,7 +334,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             int s = 0;
             uint32_t ph = 0;
             for (int t = first; ok && t < total; t += step) {
-                const I8Tile tl = i8_tile<FORM>(t, nb, a, splan, rank);
+                const I8Tile tl = i8_tile<FORM>(t, a, splan, rank);
                 const int a_row = tl.e * a.N + tl.ma * 128;
                 const uint32_t tx = (PAIR ? 2u : 1u) * (kATileBytes + (uint32_t)tl.b_n * kBRowBytes);
                 for (int kb = kb0; kb < kb1; kb++) {
@@ -281,7 +382,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             uint32_t ph = 0, aph = 0;
             bool ok = true, issued = false;
             for (int t = first; ok && t < total; t += step) {
-                const I8Tile tl = i8_tile<FORM>(t, nb, a, splan, rank);
+                const I8Tile tl = i8_tile<FORM>(t, a, splan, rank);
                 if (!bounded_wait(ptx::smem_u32(&ctl->tempty[acc]), aph ^ 1u, ctl, a.err)) {
                     ok = false;
                     break;
@@ -331,11 +432,11 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     } else {
         // ------------------------------------------------------------ epilogue (warps 2-9)
         const int quad = warp & 3, half = (warp - 2) >> 2;
-        float* s_sx = reinterpret_cast<float*>(smem + kI8RingBytes + kBarBytes + sizeof(SmemPlan)) + (warp - 2) * 256;
+        float* s_sx = reinterpret_cast<float*>(smem + kI8RingBytes + kBarBytes + sizeof(I8Plan)) + (warp - 2) * 256;
         int acc = 0;
         uint32_t aph = 0;
         for (int t = first; t < total; t += step) {
-            const I8Tile tl = i8_tile<FORM>(t, nb, a, splan, rank);
+            const I8Tile tl = i8_tile<FORM>(t, a, splan, rank);
             // scales, fetched before the accumulator wait: a channel a lane, the tile's rows in shared memory
             const int ch0 = tl.ma * 128 + quad * 32, ch = ch0 + lane;
             const float sw = (FORM != I8_SPLIT && ch < a.N) ? __ldg(a.sw + (size_t)tl.e * a.N + ch) : 0.f;
@@ -404,7 +505,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         // every CTA of the cluster adds a share of the tile: the flattened (column,
         // 4 channels) items, dealt over the cluster's threads
         if (first < total) {
-            const I8Tile tl = i8_tile<FORM>(first, nb, a, splan, rank);
+            const I8Tile tl = i8_tile<FORM>(first, a, splan, rank);
             const int items = tl.rows * 32;
             for (int i = rank * kI8Threads + (int)threadIdx.x; i < items; i += split * kI8Threads) {
                 const int col = i >> 5, c4 = (i & 31) * 4;

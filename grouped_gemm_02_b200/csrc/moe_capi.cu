@@ -1428,9 +1428,6 @@ int norm_entry(const moe_bf16* x, const moe_bf16* residual, const moe_bf16* weig
     return run_norm<OUT>(a, dev->sm_count, as_stream(stream));
 }
 
-constexpr PlanShape kPlanI8{kTileRows, 64, 128, 16, 0, kTilesCap};
-constexpr PlanShape kPlanI8Pair{kTileRows, 128, 256, 32, 1, kTilesCap};
-
 // Launches a product in one of its forms; `split` CTAs share a tile in I8_SPLIT.
 int run_int8(const Int8Args& a, const void* xq, int64_t rows, const void* Wq, int64_t wrows, int form, int64_t tiles,
              int split, const DeviceState* dev, cudaStream_t st)
@@ -1585,29 +1582,24 @@ int moe_grouped_gemm_int8(const int8_t* xpq, const float* sxp, const int32_t* co
     if (T == 0) return MOE_OK;
     if (!xpq || !sxp || !counts || !offsets || !Wq || !sw || !out || !ws) return MOE_ERR_ARG;
     if (!al16(xpq) || !al16(sxp) || !al16(Wq) || !al16(sw) || !al16(out) || !al16(ws)) return MOE_ERR_ALIGN;
-    const WsLayout L = ws_layout(T, 0, 0, E, k, 0);
-    if (ws_bytes < L.ctrl_end) return MOE_ERR_WS;
+    if (ws_bytes < 256) return MOE_ERR_WS;   // the error word
     DeviceState* dev;
     if ((rc = device_setup(&dev))) return rc;
-    cudaStream_t st = as_stream(stream);
-    int32_t* plan = at<int32_t>(ws, L.plan);
     const int64_t P = T * k;
-    const int forced = policy(g_policy_pair, "MOE_GEMM_PAIR", /*invert=*/false);
-    const bool pair = dev->i8_pair_grid >= 2 && (forced >= 0 ? forced == 1 : P >= 256);
-    const PlanShape ps = pair ? kPlanI8Pair : kPlanI8;
-    if (launch(plan_kernel, dim3(1), dim3(1024), 0, st, counts, offsets, (int)E, plan, 0, (int)N, 0, 0, ps) !=
-        cudaSuccess)
-        return MOE_ERR_CUDA;
+    const bool pair = i8_grouped_pair(P, K, N, E, dev->sm_count, dev->i8_pair_grid >= 2,
+                                      policy(g_policy_pair, "MOE_GEMM_PAIR", /*invert=*/false));
     Int8Args a{};
-    a.plan = plan;
+    a.counts = counts;
+    a.offsets = offsets;
+    a.E = (int)E;
     a.T = (int)P;
     a.N = (int)N;
     a.K = (int)K;
     a.sx = sxp;
     a.sw = sw;
     a.out = reinterpret_cast<bf16*>(out);
-    a.err = at<uint32_t>(ws, L.err);
-    return run_int8(a, xpq, P, Wq, E * N, pair ? I8_PAIR : I8_SINGLE, dev->sm_count, 1, dev, st);
+    a.err = static_cast<uint32_t*>(ws);
+    return run_int8(a, xpq, P, Wq, E * N, pair ? I8_PAIR : I8_SINGLE, dev->sm_count, 1, dev, as_stream(stream));
 }
 
 int moe_permute_int8(const int32_t* topk_idx, const int8_t* xq, const float* sx, int64_t T, int64_t d, int64_t E,
