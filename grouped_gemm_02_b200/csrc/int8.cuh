@@ -38,8 +38,9 @@ namespace moe {
 constexpr int kI8MaxK = 1 << 16;
 constexpr int kI8Epilogues = 8;                  // epilogue warps
 constexpr int kI8Threads = 64 + 32 * kI8Epilogues;
-constexpr int kI8RingBytes = 200 * 1024;
-constexpr int kI8ScaleBytes = kI8Epilogues * 256 * 4;       // each epilogue warp's copy of its tile's row scales
+constexpr int kI8RingBytes = 192 * 1024;
+constexpr int kI8ScaleBytes = 2 * 256 * 4;       // the tile's row scales, for each half of the epilogue warps
+constexpr int kI8TurnBytes = 2 * 2 * 16 * 256;   // [half][buffer][16 rows][128 channels] bf16
 
 // The tiles of a grouped product, built by every CTA for itself from counts and
 // offsets: one block for each expert with rows, heaviest first, cut into `units`
@@ -51,7 +52,7 @@ struct I8Plan {
     int tb[kMaxExperts + 1];        // prefix of units
     int nb, widest, cap;
 };
-constexpr int kI8SmemBytes = 1024 + kI8RingBytes + kBarBytes + (int)sizeof(I8Plan) + kI8ScaleBytes;
+constexpr int kI8SmemBytes = 1024 + kI8RingBytes + kBarBytes + (int)sizeof(I8Plan) + kI8ScaleBytes + kI8TurnBytes;
 static_assert(kI8SmemBytes <= 227 * 1024, "shared memory budget");
 static_assert(sizeof(I8Plan) % 16 == 0 && kBarBytes % 16 == 0, "the scales are read as float4");
 static_assert(128 * 256 * 4 <= kI8RingBytes, "the int32 tile of I8_SPLIT reuses the ring");
@@ -432,25 +433,26 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     } else {
         // ------------------------------------------------------------ epilogue (warps 2-9)
         const int quad = warp & 3, half = (warp - 2) >> 2;
-        float* s_sx = reinterpret_cast<float*>(smem + kI8RingBytes + kBarBytes + sizeof(I8Plan)) + (warp - 2) * 256;
+        uint8_t* s_half = smem + kI8RingBytes + kBarBytes + sizeof(I8Plan);
+        float* s_sx = reinterpret_cast<float*>(s_half) + half * 256;
+        uint4* s_turn = reinterpret_cast<uint4*>(s_half + kI8ScaleBytes + half * (kI8TurnBytes / 2));
+        uint32_t chunks = 0;    // 16-column chunks so far: the turn buffer alternates across tiles too
         int acc = 0;
         uint32_t aph = 0;
         for (int t = first; t < total; t += step) {
             const I8Tile tl = i8_tile<FORM>(t, a, splan, rank);
             // scales, fetched before the accumulator wait: a channel a lane, the tile's rows in shared memory
-            const int ch0 = tl.ma * 128 + quad * 32, ch = ch0 + lane;
+            const int ch = tl.ma * 128 + quad * 32 + lane;
             const float sw = (FORM != I8_SPLIT && ch < a.N) ? __ldg(a.sw + (size_t)tl.e * a.N + ch) : 0.f;
             if (FORM != I8_SPLIT) {
-                __syncwarp();       // the last tile's scales have been read
-                for (int i = lane; i < tl.n_mma; i += 32) {
-                    const int col = 2 * (i & ~15) + 16 * half + (i & 15);   // the columns this warp takes
-                    if (col >= tl.n_mma) break;
-                    s_sx[col] = col < tl.rows ? __ldg(a.sx + tl.row0 + col) : 0.f;
-                }
-                __syncwarp();
+                // the half's four warps share the scales; the last tile's were read before
+                // its last chunk's barrier
+                for (int i = quad * 32 + lane; i < tl.n_mma; i += 128)
+                    s_sx[i] = i < tl.rows ? __ldg(a.sx + tl.row0 + i) : 0.f;
             }
             const bool ok = bounded_wait(ptx::smem_u32(&ctl->tfull[acc]), aph, ctl, a.err);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            // the half leaves together: its warps meet at the chunks' barriers
+            if (ptx::named_barrier_or(1 + half, 128, !ok)) break;
             ptx::tc_fence_after();
             const uint32_t taddr = tmem_base + (uint32_t)acc * 256u + ((uint32_t)(quad * 32) << 16);
             for (int c0 = 16 * half; c0 < tl.n_mma; c0 += 32) {
@@ -478,12 +480,23 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                     }
                     uint4 o[2];
                     i8_turn16(w, o, lane);
-                    const int oc = ch0 + (lane >> 3) * 8;
+                    // through shared memory into rows of 128 channels: a warp stores four whole
+                    // 256-byte rows (64-byte pieces from each quadrant's warp cost 15 to 20% of
+                    // the product at K = 2048).  16-byte units are swizzled by the row.
+                    uint4* buf = s_turn + (chunks++ & 1u) * 256;
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
-                        const int col = c0 + 8 * h + (lane & 7);
+                        const int r = 8 * h + (lane & 7);
+                        buf[r * 16 + ((quad * 4 + (lane >> 3)) ^ (r & 7))] = o[h];
+                    }
+                    ptx::named_barrier(1 + half, 128);
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const int r = 4 * quad + 2 * h + (lane >> 4), u = lane & 15;
+                        const int col = c0 + r, oc = tl.ma * 128 + u * 8;
                         if (col < tl.rows && oc < a.N)   // N % 8 == 0: all 8 channels or none
-                            *reinterpret_cast<uint4*>(a.out + (size_t)(tl.row0 + col) * a.N + oc) = o[h];
+                            *reinterpret_cast<uint4*>(a.out + (size_t)(tl.row0 + col) * a.N + oc) =
+                                buf[r * 16 + (u ^ (r & 7))];
                     }
                 }
             }
