@@ -183,6 +183,12 @@ int device_setup(DeviceState** out)
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmemBytes) != cudaSuccess ||
                 cudaFuncSetAttribute(grouped_gemm_kernel<MODE_FUSED, true>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmemBytes) != cudaSuccess ||
+                cudaFuncSetAttribute(rmsnorm_grad_kernel<2, 512>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kNormGradSmemBytes) != cudaSuccess ||
+                cudaFuncSetAttribute(rmsnorm_grad_kernel<4, 512>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kNormGradSmemBytes) != cudaSuccess ||
+                cudaFuncSetAttribute(rmsnorm_grad_kernel<4, 1024>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kNormGradSmemBytes) != cudaSuccess ||
                 cudaFuncSetAttribute(int8_gemm_kernel<I8_SINGLE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      kI8SmemBytes) != cudaSuccess ||
                 cudaFuncSetAttribute(int8_gemm_kernel<I8_PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1516,9 +1522,11 @@ int moe_rmsnorm_backward(const moe_bf16* dy, const moe_bf16* xsum, const moe_bf1
     a.T = T;
     a.d = (int)d;
     a.eps = eps;
-    auto kernel = s.vpt == 2 ? rmsnorm_grad_kernel<2> : rmsnorm_grad_kernel<4>;
-    if (launch(kernel, dim3((unsigned)(groups / s.groups)), dim3(s.warps * s.groups * 32), 0, st, a, s.warps) !=
-        cudaSuccess)
+    auto kernel = s.vpt == 2 ? rmsnorm_grad_kernel<2, 512>
+                  : s.warps <= 16 ? rmsnorm_grad_kernel<4, 512> : rmsnorm_grad_kernel<4, 1024>;
+    const int stages = norm_grad_stages(s);
+    if (launch(kernel, dim3((unsigned)(groups / s.groups)), dim3(s.warps * s.groups * 32),
+               (size_t)stages * norm_grad_stage_bytes(s), st, a, s.warps, stages) != cudaSuccess)
         return MOE_ERR_CUDA;
     return status_of(launch(norm_dw_kernel, dim3((unsigned)((d + 31) / 32)), dim3(256), 0, st,
                             (const float*)a.partials, groups, (int)d, dweight));

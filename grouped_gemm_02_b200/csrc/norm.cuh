@@ -316,9 +316,11 @@ struct NormGradArgs {
 
 constexpr int kNormGradCtas = 296;   // two a B200 SM; fixed, so that the workspace and every bit follow from the sizes
 
-// Layout of the gradient's rows: 2 vectors a thread up to d = 16384 (the
-// columns' dw, 8 floats a vector, stay in registers), 4 above.
-__host__ __device__ inline RowShape norm_grad_shape(int d) { return row_shape(d / 8, d <= 16384 ? 2 : 4); }
+// Layout of the gradient's rows: 2 vectors a thread up to d = 8192 and 4 above,
+// so that a row takes at most 512 threads up to d = 16384 and a thread may hold
+// 128 registers (its columns' dw are 8 a vector).  Wider rows take 1024 threads
+// of 64 registers, which then read the weight again for every row.
+__host__ __device__ inline RowShape norm_grad_shape(int d) { return row_shape(d / 8, d <= 8192 ? 2 : 4); }
 
 __host__ __device__ inline int64_t norm_grad_groups(int64_t T, int d)
 {
@@ -327,9 +329,27 @@ __host__ __device__ inline int64_t norm_grad_groups(int64_t T, int d)
     return (ctas < kNormGradCtas ? ctas : kNormGradCtas) * s.groups;
 }
 
-template <int VPT>
-__global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const NormGradArgs a, int warps)
+// Rows in flight a group: every thread copies its own vectors of s, dy and dxsum
+// into its own slots of shared memory (cp.async, no barrier), `stages` rows deep.
+// Two CTAs an SM share about 200 KB, so a CTA takes as many stages as fit 100 KB,
+// at most 4, and one that needs more than that for two runs alone on its SM.
+// Without the copies ahead (loads straight into registers) an SM's loads stop
+// while its rows are reduced: T=4099 d=7168 78 us against 49.
+__host__ __device__ inline int norm_grad_stage_bytes(const RowShape& s) { return s.groups * s.warps * 32 * s.vpt * 48; }
+
+__host__ __device__ inline int norm_grad_stages(const RowShape& s)
 {
+    const int bytes = norm_grad_stage_bytes(s);
+    const int n = 100 * 1024 / bytes;
+    return n >= 4 ? 4 : n >= 2 ? n : 2 * bytes <= 200 * 1024 ? 2 : 1;
+}
+
+constexpr int kNormGradSmemBytes = 200 * 1024;   // the most any shape takes (d = 16384: two stages of 512 x 4 vectors)
+
+template <int VPT, int MAXT>
+__global__ void __launch_bounds__(MAXT) rmsnorm_grad_kernel(const NormGradArgs a, int warps, int stages)
+{
+    extern __shared__ __align__(16) uint8_t s_rows[];
     __shared__ float s_red[2][2][32];
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
@@ -338,30 +358,49 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const NormGradArgs a
     const int group = (int)threadIdx.x / gt, ti = (int)threadIdx.x - group * gt;
     const int64_t stride = (int64_t)gridDim.x * per_cta, g0 = (int64_t)blockIdx.x * per_cta + group;
     const int nvec = a.d / 8;
+    const int nt = blockDim.x;
+    uint4* slots = reinterpret_cast<uint4*>(s_rows) + threadIdx.x;    // [stage][tensor][i] of this thread, nt apart
+    constexpr bool kKeepW = MAXT <= 512;
+    auto weight = [&](int i) {
+        const int v = i * gt + ti;
+        return v < nvec ? __ldg(reinterpret_cast<const uint4*>(a.weight) + v) : make_uint4(0u, 0u, 0u, 0u);
+    };
     float dw[VPT][8];
-    uint4 w[VPT];
+    uint4 w[kKeepW ? VPT : 1];
 #pragma unroll
     for (int i = 0; i < VPT; i++) {
-        const int v = i * gt + ti;
-        w[i] = v < nvec ? __ldg(reinterpret_cast<const uint4*>(a.weight) + v) : make_uint4(0u, 0u, 0u, 0u);
+        if (kKeepW) w[i] = weight(i);
 #pragma unroll
         for (int j = 0; j < 8; j++) dw[i][j] = 0.f;
     }
-    int par = 0;
-    for (int64_t row = g0; row < a.T; row += stride, par ^= 1) {
-        uint4 us[VPT], ug[VPT], ur[VPT];
+    auto fetch = [&](int64_t row, int st) {
+        if (row < a.T) {
 #pragma unroll
-        for (int i = 0; i < VPT; i++) {
-            const int v = i * gt + ti;
-            const bool in = v < nvec;
-            us[i] = in ? reinterpret_cast<const uint4*>(a.s + row * a.d)[v] : make_uint4(0u, 0u, 0u, 0u);
-            ug[i] = in ? reinterpret_cast<const uint4*>(a.dy + row * a.d)[v] : make_uint4(0u, 0u, 0u, 0u);
-            ur[i] = in && a.dxsum ? reinterpret_cast<const uint4*>(a.dxsum + row * a.d)[v] : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < VPT; i++) {
+                const int v = i * gt + ti;
+                if (v < nvec) {
+                    uint4* p = slots + (st * 3 * VPT + i) * nt;
+                    ptx::cp_async16(p, reinterpret_cast<const uint4*>(a.s + row * a.d) + v);
+                    ptx::cp_async16(p + VPT * nt, reinterpret_cast<const uint4*>(a.dy + row * a.d) + v);
+                    if (a.dxsum) ptx::cp_async16(p + 2 * VPT * nt, reinterpret_cast<const uint4*>(a.dxsum + row * a.d) + v);
+                }
+            }
         }
+        ptx::cp_async_commit();      // an empty group past the last row keeps the count
+    };
+    for (int st = 0; st < stages - 1; st++) fetch(g0 + st * stride, st);
+    int par = 0, st = 0;
+    for (int64_t row = g0; row < a.T; row += stride, par ^= 1) {
+        // the slot of the row before last is free: this thread has used its values
+        fetch(row + (stages - 1) * stride, st == 0 ? stages - 1 : st - 1);
+        ptx::cp_async_wait(stages - 1);
+        const uint4* mine = slots + st * 3 * VPT * nt;
+        if (++st == stages) st = 0;
         float ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; i++) {
-            const f8 s = unpack8(us[i]), g = unpack8(ug[i]), wf = unpack8(w[i]);
+            if (i * gt + ti >= nvec) continue;
+            const f8 s = unpack8(mine[i * nt]), g = unpack8(mine[(VPT + i) * nt]), wf = unpack8(kKeepW ? w[i] : weight(i));
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 ss = fmaf(s.v[j], s.v[j], ss);
@@ -386,17 +425,24 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const NormGradArgs a
 #pragma unroll
         for (int i = 0; i < VPT; i++) {
             const int v = i * gt + ti;
-            const f8 s = unpack8(us[i]), g = unpack8(ug[i]), wf = unpack8(w[i]), r = unpack8(ur[i]);
+            if (v >= nvec) continue;
+            const f8 s = unpack8(mine[i * nt]), g = unpack8(mine[(VPT + i) * nt]), wf = unpack8(kKeepW ? w[i] : weight(i));
             f8 o;
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 const float n = s.v[j] * rstd;
-                o.v[j] = (g.v[j] * wf.v[j] - n * m) * rstd + r.v[j];
+                o.v[j] = (g.v[j] * wf.v[j] - n * m) * rstd;
                 dw[i][j] = fmaf(g.v[j], n, dw[i][j]);
             }
-            if (v < nvec) reinterpret_cast<uint4*>(a.dx + row * a.d)[v] = pack8(o);
+            if (a.dxsum) {
+                const f8 r = unpack8(mine[(2 * VPT + i) * nt]);
+#pragma unroll
+                for (int j = 0; j < 8; j++) o.v[j] += r.v[j];
+            }
+            reinterpret_cast<uint4*>(a.dx + row * a.d)[v] = pack8(o);
         }
     }
+    ptx::cp_async_wait(0);
 #pragma unroll
     for (int i = 0; i < VPT; i++) {
         const int v = i * gt + ti;

@@ -462,6 +462,24 @@ __device__ __forceinline__ bool named_barrier_or(int id, int threads, bool v)
     return r != 0;
 }
 
+// ---------------------------------------------------------------- asynchronous copies (cp.async)
+// 16 bytes global -> shared, past L1; complete after a wait on its group.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Wait until at most `left` (0..3) of this thread's groups are in flight.
+__device__ __forceinline__ void cp_async_wait(int left)
+{
+    if (left >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (left == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (left == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- grid dependency (PDL)
 __device__ __forceinline__ void grid_dep_wait()
 {
