@@ -1487,7 +1487,7 @@ int moe_rmsnorm_int8(const moe_bf16* x, const moe_bf16* residual, const moe_bf16
 int moe_rmsnorm_backward_workspace_size(int64_t T, int64_t d, size_t* bytes)
 {
     if (!bytes || T < 0 || T >= (int64_t(1) << 31) || d <= 0 || d > kNormMaxD) return MOE_ERR_ARG;
-    *bytes = align_up((size_t)norm_grad_groups(T, (int)d) * d * 4, 256);
+    *bytes = align_up((size_t)norm_grad_ctas(T, (int)d) * d * 4, 256);
     return MOE_OK;
 }
 
@@ -1508,8 +1508,8 @@ int moe_rmsnorm_backward(const moe_bf16* dy, const moe_bf16* xsum, const moe_bf1
     }
     if (!dy || !xsum || !weight || !dx || !ws) return MOE_ERR_ARG;
     if (!al16(dy) || !al16(xsum) || !al16(weight) || !al16(dxsum) || !al16(dx) || !al16(ws)) return MOE_ERR_ALIGN;
-    const int64_t groups = norm_grad_groups(T, (int)d);
-    if (ws_bytes < (size_t)groups * d * 4) return MOE_ERR_WS;
+    const int64_t ctas = norm_grad_ctas(T, (int)d);
+    if (ws_bytes < (size_t)ctas * d * 4) return MOE_ERR_WS;
     if ((rc = device_setup(&dev))) return rc;
     const RowShape s = norm_grad_shape((int)d);
     NormGradArgs a{};
@@ -1525,11 +1525,11 @@ int moe_rmsnorm_backward(const moe_bf16* dy, const moe_bf16* xsum, const moe_bf1
     auto kernel = s.vpt == 2 ? rmsnorm_grad_kernel<2, 512>
                   : s.warps <= 16 ? rmsnorm_grad_kernel<4, 512> : rmsnorm_grad_kernel<4, 1024>;
     const int stages = norm_grad_stages(s);
-    if (launch(kernel, dim3((unsigned)(groups / s.groups)), dim3(s.warps * s.groups * 32),
+    if (launch(kernel, dim3((unsigned)ctas), dim3(s.warps * s.groups * 32),
                (size_t)stages * norm_grad_stage_bytes(s), st, a, s.warps, stages) != cudaSuccess)
         return MOE_ERR_CUDA;
-    return status_of(launch(norm_dw_kernel, dim3((unsigned)((d + 31) / 32)), dim3(256), 0, st,
-                            (const float*)a.partials, groups, (int)d, dweight));
+    return status_of(launch(norm_dw_kernel, dim3((unsigned)(d / 32)), dim3(512), 0, st, (const float*)a.partials,
+                            (int)ctas, (int)d, dweight));
 }
 
 int moe_quantize_int8_rows(const moe_bf16* x, int64_t rows, int64_t cols, int8_t* q, float* scale, void* stream)
@@ -1621,7 +1621,7 @@ int moe_permute_int8(const int32_t* topk_idx, const int8_t* xq, const float* sx,
         return MOE_ERR_ARG;
     if (!al16(xq) || !al16(xpq) || !al16(ws)) return MOE_ERR_ALIGN;
     const WsLayout L = ws_layout(T, 0, 0, E, k, 0);
-    if (ws_bytes < L.ctrl_end) return MOE_ERR_WS;
+    if (ws_bytes < L.total) return MOE_ERR_WS;
     DeviceState* dev;
     if ((rc = device_setup(&dev))) return rc;
     cudaStream_t st = as_stream(stream);
@@ -1629,6 +1629,15 @@ int moe_permute_int8(const int32_t* topk_idx, const int8_t* xq, const float* sx,
     if (T * k <= kSmallPairs) {
         if (launch(permute_small_kernel, dim3(1), dim3(1024), 0, st, topk_idx, (int)(T * k), (int)E, counts, offsets,
                    perm, inv_perm, (int32_t*)nullptr, 0, 0, 0, 0, kPlanSingle, err) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    } else if (T * k <= kSortPairs) {
+        // chunks * E counts take the place of the logits: at most T * k / 512 * E < T * E of them
+        const int P = (int)(T * k), chunks = sort_chunks(P);
+        int32_t* hist = at<int32_t>(ws, L.logits);
+        if (launch(chunk_hist_kernel, dim3(chunks), dim3(kSortChunk), 0, st, topk_idx, P, (int)E, hist, err) !=
+                cudaSuccess ||
+            launch(chunk_rank_kernel, dim3(chunks), dim3(kSortChunk), 0, st, topk_idx, P, (int)E,
+                   (const int32_t*)hist, chunks, counts, offsets, perm, inv_perm) != cudaSuccess)
             return MOE_ERR_CUDA;
     } else if ((rc = run_permute(topk_idx, nullptr, (int)T, (int)d, (int)E, (int)k, counts, offsets, perm, inv_perm,
                                  nullptr, err, at<int32_t>(ws, L.block_counts), nullptr, 0, 0, 0, dev->sm_count, st,

@@ -113,11 +113,13 @@ __device__ __forceinline__ uint32_t group_umax(uint32_t v, uint32_t* slot, int g
 // The magnitude bits of the largest of 8 bf16 values (a NaN ranks above infinity), as fp32 bits.
 __device__ __forceinline__ uint32_t amax_bits8(const uint4& u)
 {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; i++) m = max(m, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
-    return m;
+    auto mag = [](uint32_t w) {
+        const uint32_t m = w & 0x7FFF7FFFu;
+        return *reinterpret_cast<const __nv_bfloat162*>(&m);
+    };
+    const __nv_bfloat162 t = __hmax2_nan(__hmax2_nan(mag(u.x), mag(u.y)), __hmax2_nan(mag(u.z), mag(u.w)));
+    const uint32_t m = *reinterpret_cast<const uint32_t*>(&t);
+    return max(m << 16, m & 0xFFFF0000u);
 }
 
 // ---------------------------------------------------------------- int8 codes
@@ -155,15 +157,27 @@ __device__ __forceinline__ uint2 int8_codes8(const uint4& u, float inv)
 // ---------------------------------------------------------------- e4m3 codes
 // 8 values of a 1 x 128 block spread over 16 consecutive lanes: the block's
 // exponent (the rule of the row quantiser in fp8.cuh) and this lane's codes.
+// amax = 1.f x 2^(x - 127): the smallest e with amax <= 448 2^e = 1.75 2^(8 + e) is
+// x - 135, one more above 1.75, held to -127 (a subnormal amax has x = 0).  The
+// quantiser's maximum passes over a NaN, and takes infinity's exponent from frexpf:
+// blocks that hold either go through its own functions.
 __device__ __forceinline__ int e4m3_block_exp(const uint4& u)
 {
-    const f8 f = unpack8(u);
-    float a = 0.f;
+    uint32_t a = amax_bits8(u);
 #pragma unroll
-    for (int i = 0; i < 8; i++) a = fmaxf(a, fabsf(f.v[i]));
+    for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+    if (a >= 0x7F800000u) {      // the same for the 16 lanes of a block
+        const unsigned lanes = 0xFFFFu << (threadIdx.x & 16);
+        const f8 f = unpack8(u);
+        float m = 0.f;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    return fp8_scale_exp(a);
+        for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(f.v[i]));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, o));
+        return fp8_scale_exp(m);
+    }
+    if (a == 0u) return 0;
+    return max(-127, (int)(a >> 23) - 135 + ((a & 0x7FFFFFu) > 0x600000u ? 1 : 0));
 }
 
 __device__ __forceinline__ uint2 e4m3_codes8(const uint4& u, int e)
@@ -299,42 +313,36 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a, int war
 //   ds = (g - n * m) * rstd (+ dxsum, the stream's own gradient)   -> dx, bf16
 //   dw = sum over rows of dy * n                                   -> fp32
 // rstd is formed again from s, which is read anyway.  Each group walks the rows
-// group, group + groups, ... and keeps its columns' dw in registers; it writes
-// them once to partials[group][d], and norm_dw_kernel adds the groups in a
-// fixed order: no atomics, the same bits in every run.
+// group, group + groups, ... and keeps its columns' dw in registers; a CTA adds
+// its groups and writes one row of partials[CTA][d], and norm_dw_kernel adds the
+// CTAs, all in a fixed order: no atomics, the same bits in every run.
 struct NormGradArgs {
     const bf16* dy;
     const bf16* s;
     const bf16* weight;
     const bf16* dxsum;      // may be null
     bf16* dx;               // may be dy or dxsum
-    float* partials;        // [groups, d]
+    float* partials;        // [CTAs, d]
     int64_t T;
     int d;
     float eps;
 };
 
-constexpr int kNormGradCtas = 296;   // two a B200 SM; fixed, so that the workspace and every bit follow from the sizes
-
-// Layout of the gradient's rows: 2 vectors a thread up to d = 8192 and 4 above,
+// Layout of the gradient's rows: 2 vectors a thread up to d = 4096 and 4 above,
 // so that a row takes at most 512 threads up to d = 16384 and a thread may hold
 // 128 registers (its columns' dw are 8 a vector).  Wider rows take 1024 threads
-// of 64 registers, which then read the weight again for every row.
-__host__ __device__ inline RowShape norm_grad_shape(int d) { return row_shape(d / 8, d <= 8192 ? 2 : 4); }
-
-__host__ __device__ inline int64_t norm_grad_groups(int64_t T, int d)
-{
-    const RowShape s = norm_grad_shape(d);
-    const int64_t ctas = (T + s.groups - 1) / s.groups;
-    return (ctas < kNormGradCtas ? ctas : kNormGradCtas) * s.groups;
-}
+// of 64 registers, which then read the weight again for every row.  Measured
+// (T=4099): d=7168 44.7 us with 4 vectors, 48.7 with 2, 66.7 with 1 -- the sums
+// over a row cost every warp the same, so few warps with much of the row each
+// are better -- and d=2048 17.4 with 2, 20.2 with 4, where a row is short.
+__host__ __device__ inline RowShape norm_grad_shape(int d) { return row_shape(d / 8, d <= 4096 ? 2 : 4); }
 
 // Rows in flight a group: every thread copies its own vectors of s, dy and dxsum
 // into its own slots of shared memory (cp.async, no barrier), `stages` rows deep.
 // Two CTAs an SM share about 200 KB, so a CTA takes as many stages as fit 100 KB,
 // at most 4, and one that needs more than that for two runs alone on its SM.
 // Without the copies ahead (loads straight into registers) an SM's loads stop
-// while its rows are reduced: T=4099 d=7168 78 us against 49.
+// while its rows are reduced: T=4099 d=7168 78 us.
 __host__ __device__ inline int norm_grad_stage_bytes(const RowShape& s) { return s.groups * s.warps * 32 * s.vpt * 48; }
 
 __host__ __device__ inline int norm_grad_stages(const RowShape& s)
@@ -342,6 +350,20 @@ __host__ __device__ inline int norm_grad_stages(const RowShape& s)
     const int bytes = norm_grad_stage_bytes(s);
     const int n = 100 * 1024 / bytes;
     return n >= 4 ? 4 : n >= 2 ? n : 2 * bytes <= 200 * 1024 ? 2 : 1;
+}
+
+// CTAs of a launch: two a B200 SM where their rows fit (T=4099 d=7168: 44.7 us
+// against 58.0 with one and twice the stages), one where they do not (T=1024
+// d=16384: 28.8 us against 35.7 with two in turn).  Fixed numbers, so that the
+// workspace and every bit of the result follow from the sizes alone.
+constexpr int kNormGradCtas = 296;
+
+__host__ __device__ inline int64_t norm_grad_ctas(int64_t T, int d)
+{
+    const RowShape s = norm_grad_shape(d);
+    const int most = norm_grad_stages(s) * norm_grad_stage_bytes(s) <= 110 * 1024 ? kNormGradCtas : kNormGradCtas / 2;
+    const int64_t ctas = (T + s.groups - 1) / s.groups;
+    return ctas < most ? ctas : most;
 }
 
 constexpr int kNormGradSmemBytes = 200 * 1024;   // the most any shape takes (d = 16384: two stages of 512 x 4 vectors)
@@ -443,37 +465,63 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_grad_kernel(const NormGradArgs a
         }
     }
     ptx::cp_async_wait(0);
+    float* part = a.partials + (int64_t)blockIdx.x * a.d;
+    if (per_cta > 1) {
+        // the groups one after the other, into the row buffer: nothing of it is in use any more
+        float* sum = reinterpret_cast<float*>(s_rows);
+        for (int g = 0; g < per_cta; g++) {
+            __syncthreads();
+            if (g != group) continue;
+#pragma unroll
+            for (int i = 0; i < VPT; i++) {
+                const int v = i * gt + ti;
+                if (v >= nvec) continue;
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    if (g > 0) dw[i][j] += sum[8 * v + j];
+                    sum[8 * v + j] = dw[i][j];
+                }
+            }
+        }
+        if (group != per_cta - 1) return;      // the last group holds the total
+    }
 #pragma unroll
     for (int i = 0; i < VPT; i++) {
         const int v = i * gt + ti;
         if (v < nvec) {
-            float4* p = reinterpret_cast<float4*>(a.partials + g0 * a.d) + 2 * v;
+            float4* p = reinterpret_cast<float4*>(part) + 2 * v;
             p[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
             p[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
         }
     }
 }
 
-// dweight[c] = sum over groups of partials[g][c], in a fixed order: a CTA of 256
-// threads takes 32 columns, 8 threads a column each every 8th group, then those
-// 8 sums in order.
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ partials, int64_t groups, int d,
+// dweight[c] = sum over CTAs of partials[g][c], in a fixed order: a CTA of 512
+// threads takes 32 columns, 16 threads a column each every 16th row (at most 19,
+// loads in flight together), then those 16 sums in order.
+__global__ void __launch_bounds__(512) norm_dw_kernel(const float* __restrict__ partials, int rows, int d,
                                                       float* __restrict__ dweight)
 {
-    __shared__ float s_part[8][33];
+    __shared__ float s_part[16][33];
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     const int cx = threadIdx.x & 31, gy = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + cx;
+    const int c = blockIdx.x * 32 + cx;      // d % 32 == 0
+    float v[(kNormGradCtas + 15) / 16];
+#pragma unroll
+    for (int i = 0; i < (kNormGradCtas + 15) / 16; i++) {
+        const int g = 16 * i + gy;
+        v[i] = g < rows ? partials[(int64_t)g * d + c] : 0.f;
+    }
     float acc = 0.f;
-    if (c < d)
-        for (int64_t g = gy; g < groups; g += 8) acc += partials[g * d + c];
+#pragma unroll
+    for (int i = 0; i < (kNormGradCtas + 15) / 16; i++) acc += v[i];
     s_part[gy][cx] = acc;
     __syncthreads();
-    if (gy == 0 && c < d) {
+    if (gy == 0) {
         float t = s_part[0][cx];
 #pragma unroll
-        for (int i = 1; i < 8; i++) t += s_part[i][cx];
+        for (int i = 1; i < 16; i++) t += s_part[i][cx];
         dweight[c] = t;
     }
 }

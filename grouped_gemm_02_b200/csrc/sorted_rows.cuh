@@ -17,6 +17,7 @@
 
 #include "common.cuh"
 #include "norm.cuh"
+#include "permute.cuh"
 #include "ptx.cuh"
 
 namespace moe {
@@ -28,7 +29,105 @@ __device__ __forceinline__ int pair_pos(const int32_t* inv_perm, int64_t q, int6
     return (pos >= 0 && pos < P) ? pos : -1;
 }
 
-// ---------------------------------------------------------------- sort (int8 rows with a scale each)
+// ---------------------------------------------------------------- sort: positions
+// Stable positions of up to kSortPairs pairs in two launches, 1024 pairs a CTA:
+//   chunk_hist_kernel   hist[b][e] = pairs of expert e in chunk b
+//   chunk_rank_kernel   every CTA adds up hist for itself: an expert's total (and
+//                       from the totals its offset) and its pairs in earlier
+//                       chunks; then pos = offset + earlier + rank in the chunk
+// A chunk's CTA reads all of hist (chunks x E counts, from L2), which takes the
+// place of a scan in a launch of its own; past kSortPairs that costs more than
+// the scan and the general path (run_permute) runs.
+constexpr int kSortChunk = 1024;
+constexpr int64_t kSortPairs = int64_t(1) << 18;
+
+__host__ __device__ inline int sort_chunks(int64_t P) { return (int)((P + kSortChunk - 1) / kSortChunk); }
+
+__global__ void __launch_bounds__(kSortChunk) chunk_hist_kernel(const int32_t* __restrict__ idx, int P, int E,
+                                                                int32_t* __restrict__ hist, uint32_t* __restrict__ err)
+{
+    __shared__ int32_t cnt[kMaxExperts];
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int tid = threadIdx.x, q = blockIdx.x * kSortChunk + tid;
+    const int e = q < P ? idx[q] : -1;
+    if (tid < E) cnt[tid] = 0;
+    __syncthreads();
+    const bool in = e >= 0 && e < E;
+    if (q < P && !in) atomicOr(err, DEVERR_EXPERT_RANGE);
+    // one addition for the lanes that share an expert: a hot expert takes most of a chunk
+    const unsigned peers = __match_any_sync(0xffffffffu, in ? e : -1);
+    if (in && (tid & 31) == __ffs(peers) - 1) atomicAdd(&cnt[e], __popc(peers));
+    __syncthreads();
+    if (tid < E) hist[blockIdx.x * E + tid] = cnt[tid];
+}
+
+__global__ void __launch_bounds__(kSortChunk) chunk_rank_kernel(const int32_t* __restrict__ idx, int P, int E,
+                                                                const int32_t* __restrict__ hist, int chunks,
+                                                                int32_t* __restrict__ counts,
+                                                                int32_t* __restrict__ offsets,
+                                                                int32_t* __restrict__ perm,
+                                                                int32_t* __restrict__ inv_perm)
+{
+    __shared__ __align__(16) uint8_t s_wcnt[32][kMaxExperts];   // pairs of a warp (at most 32) by expert
+    __shared__ int s_sum[2][kSortChunk];
+    __shared__ int s_base[kMaxExperts];
+    __shared__ int warp_sums[32];
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, chunk = blockIdx.x;
+    const int q = chunk * kSortChunk + tid;
+    int e = q < P ? idx[q] : -1;
+    if (e < 0 || e >= E) {
+        if (q < P) inv_perm[q] = -1;
+        e = -1;
+    }
+    reinterpret_cast<uint4*>(&s_wcnt[0][0])[tid] = make_uint4(0, 0, 0, 0);   // 1024 x 16 B = the whole table
+    // totals and earlier pairs by expert: `parts` threads an expert, each every parts-th chunk
+    int e2 = 32;
+    while (e2 < E) e2 *= 2;
+    const int parts = kSortChunk / e2, pe = tid & (e2 - 1), pp = tid / e2;
+    int total = 0, before = 0;
+    if (pe < E) {
+#pragma unroll 4
+        for (int b = pp; b < chunks; b += parts) {
+            const int v = __ldg(hist + b * E + pe);
+            total += v;
+            before += b < chunk ? v : 0;
+        }
+    }
+    s_sum[0][tid] = total;
+    s_sum[1][tid] = before;
+    __syncthreads();
+    const unsigned peers = __match_any_sync(0xffffffffu, e);
+    const int rank = __popc(peers & ((1u << lane) - 1u));
+    if (e >= 0 && lane == __ffs(peers) - 1) s_wcnt[warp][e] = (uint8_t)__popc(peers);
+    total = before = 0;
+    if (tid < E) {
+        for (int i = 0; i < parts; i++) {
+            total += s_sum[0][i * e2 + tid];
+            before += s_sum[1][i * e2 + tid];
+        }
+    }
+    const int incl = block_inclusive_scan(total, warp_sums);
+    if (tid < E) {
+        s_base[tid] = incl - total + before;
+        if (chunk == 0) {
+            counts[tid] = total;
+            offsets[tid] = incl - total;
+            if (tid == E - 1) offsets[E] = incl;
+        }
+    }
+    __syncthreads();
+    if (e >= 0) {
+        int pos = s_base[e] + rank;
+        for (int w = 0; w < warp; w++) pos += s_wcnt[w][e];
+        perm[pos] = q;
+        inv_perm[q] = pos;
+    }
+}
+
+// ---------------------------------------------------------------- sort: int8 rows with a scale each
 // One warp per (token, 512-byte chunk of the row): a 16-byte vector per lane,
 // then its k stores; the first chunk's warp also writes the scales.
 __global__ void __launch_bounds__(256) gather_rows_int8_kernel(const uint8_t* __restrict__ xq,

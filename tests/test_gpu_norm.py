@@ -84,6 +84,23 @@ def test_rmsnorm_fp8_is_the_quantised_norm(T, d, with_residual):
         assert torch.equal(xsum[0], s)
 
 
+def test_rmsnorm_fp8_blocks_at_the_edges():
+    """Block maxima around 1.75 times a power of two, subnormal and non-finite values: the quantiser's codes and
+    scales.  A weight of ones and one row size leave y = x / rms, so the blocks' values are set by the weight."""
+    d = 2048
+    x = torch.ones(4, d, dtype=torch.bfloat16)
+    w = torch.ones(d)
+    top = [448.0, 449.0, 450.0, 447.0, 1.75, 1.7578125, 3.5, 2.0 ** -120, 2.0 ** -126, 2.0 ** -130, 3e38, 0.0, 1.0]
+    for b, v in enumerate(top):
+        w[128 * b:128 * (b + 1)] = torch.linspace(-1, 1, 128) * v
+    w[128 * 13 + 5], w[128 * 14 + 7], w[128 * 15 + 9] = float("nan"), float("inf"), float("-inf")
+    w = w.to(torch.bfloat16).to(DEV)
+    y = moe.moe_rmsnorm(x.to(DEV), w, 1e-30)
+    q, sc = moe.moe_rmsnorm_fp8(x.to(DEV), w, 1e-30)
+    rq, rs = moe.moe_quantize_fp8_rows(y)
+    assert torch.equal(sc, rs) and torch.equal(q, rq)
+
+
 @pytest.mark.parametrize("T,d", SIZES)
 @pytest.mark.parametrize("with_residual", [False, True])
 def test_rmsnorm_int8_is_the_quantised_norm(T, d, with_residual):
