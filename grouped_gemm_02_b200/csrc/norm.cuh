@@ -111,15 +111,15 @@ __device__ __forceinline__ uint32_t group_umax(uint32_t v, uint32_t* slot, int g
 }
 
 // The magnitude bits of the largest of 8 bf16 values (a NaN ranks above infinity), as fp32 bits.
+// Integer maxima, one value at a time: with packed bf16 maxima the int8 norm of T=16384
+// d=7168 took 147 us against 132.
 __device__ __forceinline__ uint32_t amax_bits8(const uint4& u)
 {
-    auto mag = [](uint32_t w) {
-        const uint32_t m = w & 0x7FFF7FFFu;
-        return *reinterpret_cast<const __nv_bfloat162*>(&m);
-    };
-    const __nv_bfloat162 t = __hmax2_nan(__hmax2_nan(mag(u.x), mag(u.y)), __hmax2_nan(mag(u.z), mag(u.w)));
-    const uint32_t m = *reinterpret_cast<const uint32_t*>(&t);
-    return max(m << 16, m & 0xFFFF0000u);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) m = max(m, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
+    return m;
 }
 
 // ---------------------------------------------------------------- int8 codes

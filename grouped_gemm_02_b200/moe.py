@@ -449,23 +449,35 @@ def _rows_of(t: torch.Tensor, name: str):
     return t.shape
 
 
-def _empty(stream, *specs, make=torch.empty):
-    """New tensors (shape, dtype) on the current device, owned by the stream that will write them."""
+def _check_stream(stream) -> None:
     dev = torch.cuda.current_device()
-    if stream is None:
-        return [make(shape, dtype=dt, device=dev) for shape, dt in specs]
     _need(stream.device_index == dev, f"stream: expected one of cuda:{dev}, got one of {stream.device}")
-    with torch.cuda.stream(stream):
-        return [make(shape, dtype=dt, device=dev) for shape, dt in specs]
+
+
+def _new(stream, like: torch.Tensor, shape=None, dtype=None) -> torch.Tensor:
+    """A new tensor on the device of ``like`` (which has been checked), owned by the stream that will write it;
+    of its shape and dtype where none is given."""
+    if stream is not None:
+        _check_stream(stream)
+        with torch.cuda.stream(stream):
+            return _new(None, like, shape, dtype)
+    if shape is None:
+        return torch.empty_like(like, dtype=dtype)
+    return like.new_empty(shape, dtype=dtype)
+
+
+# The handle of the current stream of a device, without the Python object around it (0.1 us instead of 3).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _queue(stream) -> int:
     """The handle of the stream the work goes to: the given one, or the current device's current stream."""
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    dev = torch.cuda.current_device()
-    _need(stream.device_index == dev, f"stream: expected one of cuda:{dev}, got one of {stream.device}")
-    return stream.cuda_stream
+    if stream is not None:
+        _check_stream(stream)
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -473,20 +485,19 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _norm_args(x, weight, residual, xsum, y, stream):
-    T, d = _rows_of(x, "x")
-    rows = (T, d)
+    T, d = rows = _rows_of(x, "x")
     named = [(x, rows, "x"), (weight, (d,), "weight")]
     if residual is not None:
         named.append((residual, rows, "residual"))
-        if xsum is None:
-            (xsum,) = _empty(stream, (rows, torch.bfloat16))
-        else:
-            named.append((xsum, rows, "xsum"))
     else:
         _need(xsum is None, "xsum is the sum with a residual; there is none")
+    if xsum is not None:
+        named.append((xsum, rows, "xsum"))
     if y is not None:
         named.append((y, rows, "y"))
     _tensors(torch.bfloat16, *named)
+    if residual is not None and xsum is None:
+        xsum = _new(stream, x)
     return T, d, xsum
 
 
@@ -494,7 +505,7 @@ def moe_rmsnorm(x, weight, eps: float, residual=None, xsum=None, y=None, stream=
     """y = rmsnorm(x) * weight; with a residual, (rmsnorm(x + residual) * weight, x + residual)."""
     T, d, xsum = _norm_args(x, weight, residual, xsum, y, stream)
     if y is None:
-        (y,) = _empty(stream, ((T, d), torch.bfloat16))
+        y = _new(stream, x)
     _call("moe_rmsnorm", _ptr(x), _ptr(residual), _ptr(weight), T, d, eps, _ptr(xsum), _ptr(y), _queue(stream))
     return y if residual is None else (y, xsum)
 
@@ -503,7 +514,7 @@ def moe_rmsnorm_fp8(x, weight, eps: float, residual=None, xsum=None, y=None, str
     """moe_rmsnorm with e4m3 codes and 1 x 128 scales: (q, scales) or, with a residual, (q, scales, xsum).
     ``y`` (optional, given by the caller) also receives the bf16 result."""
     T, d, xsum = _norm_args(x, weight, residual, xsum, y, stream)
-    q, sc = _empty(stream, ((T, d), torch.uint8), ((T, d // 128), torch.float32))
+    q, sc = _new(stream, x, dtype=torch.uint8), _new(stream, x, (T, d // 128), torch.float32)
     _call("moe_rmsnorm_fp8", _ptr(x), _ptr(residual), _ptr(weight), T, d, eps, _ptr(xsum), _ptr(y), _ptr(q), _ptr(sc),
           _queue(stream))
     return (q, sc) if residual is None else (q, sc, xsum)
@@ -513,7 +524,7 @@ def moe_rmsnorm_int8(x, weight, eps: float, residual=None, xsum=None, y=None, st
     """moe_rmsnorm with int8 codes and one scale a row: (q, scale) or, with a residual, (q, scale, xsum).
     ``y`` (optional, given by the caller) also receives the bf16 result."""
     T, d, xsum = _norm_args(x, weight, residual, xsum, y, stream)
-    q, sc = _empty(stream, ((T, d), torch.int8), ((T,), torch.float32))
+    q, sc = _new(stream, x, dtype=torch.int8), _new(stream, x, (T,), torch.float32)
     _call("moe_rmsnorm_int8", _ptr(x), _ptr(residual), _ptr(weight), T, d, eps, _ptr(xsum), _ptr(y), _ptr(q), _ptr(sc),
           _queue(stream))
     return (q, sc) if residual is None else (q, sc, xsum)
@@ -529,8 +540,7 @@ def moe_rmsnorm_backward(dy, xsum, weight, eps: float, dxsum=None, dx=None, dwei
     """(dx, dweight) of moe_rmsnorm: dx [T,d] bf16 (of x and of residual alike), dweight [d] fp32.
     ``dxsum``: the gradient that reaches the stream itself.  ``ws``: a uint8 tensor of
     moe_rmsnorm_backward_workspace_size bytes, made here when not given."""
-    T, d = _rows_of(dy, "dy")
-    rows = (T, d)
+    T, d = rows = _rows_of(dy, "dy")
     named = [(dy, rows, "dy"), (xsum, rows, "xsum"), (weight, (d,), "weight")]
     if dxsum is not None:
         named.append((dxsum, rows, "dxsum"))
@@ -542,11 +552,11 @@ def moe_rmsnorm_backward(dy, xsum, weight, eps: float, dxsum=None, dx=None, dwei
     if ws is not None:
         _tensors(torch.uint8, (ws, (ws.numel(),), "ws"))
     if dx is None:
-        (dx,) = _empty(stream, (rows, torch.bfloat16))
+        dx = _new(stream, dy)
     if dweight is None:
-        (dweight,) = _empty(stream, ((d,), torch.float32))
+        dweight = _new(stream, dy, (d,), torch.float32)
     if ws is None:
-        (ws,) = _empty(stream, ((moe_rmsnorm_backward_workspace_size(T, d),), torch.uint8))
+        ws = _new(stream, dy, (moe_rmsnorm_backward_workspace_size(T, d),), torch.uint8)
     _call("moe_rmsnorm_backward", _ptr(dy), _ptr(xsum), _ptr(weight), _ptr(dxsum), T, d, eps, _ptr(dx), _ptr(dweight),
           _ptr(ws), ws.numel(), _queue(stream))
     return dx, dweight
@@ -558,7 +568,7 @@ def moe_quantize_int8_rows(x: torch.Tensor, stream=None):
     _tensors(torch.bfloat16, (x, x.shape, "x"))
     Cc = x.shape[-1]
     R = x.numel() // Cc if Cc else 0
-    q, sc = _empty(stream, (x.shape, torch.int8), (x.shape[:-1], torch.float32))
+    q, sc = _new(stream, x, dtype=torch.int8), _new(stream, x, x.shape[:-1], torch.float32)
     _call("moe_quantize_int8_rows", _ptr(x), R, Cc, _ptr(q), _ptr(sc), _queue(stream))
     return q, sc
 
@@ -570,7 +580,7 @@ def moe_gemm_int8(xq, sx, Wq, sw, ws: torch.Tensor, out=None, stream=None):
     _tensors(torch.float32, (sx, (T,), "sx"), (sw, (N,), "sw"))
     _tensors(torch.uint8, (ws, (ws.numel(),), "ws"))
     if out is None:
-        (out,) = _empty(stream, ((T, N), torch.bfloat16))
+        out = _new(stream, xq, (T, N), torch.bfloat16)
     else:
         _tensors(torch.bfloat16, (out, (T, N), "out"))
     _call("moe_gemm_int8", _ptr(xq), _ptr(sx), _ptr(Wq), _ptr(sw), T, K, N, _ptr(out), _ptr(ws), ws.numel(),
@@ -590,7 +600,7 @@ def moe_grouped_gemm_int8(xpq, sxp, counts, offsets, Wq, sw, T: int, k: int, ws:
     _tensors(torch.int32, (counts, (E,), "counts"), (offsets, (E + 1,), "offsets"))
     _tensors(torch.uint8, (ws, (ws.numel(),), "ws"))
     if out is None:
-        (out,) = _empty(stream, ((P, N), torch.bfloat16))
+        out = _new(stream, xpq, (P, N), torch.bfloat16)
     else:
         _tensors(torch.bfloat16, (out, (P, N), "out"))
     _call("moe_grouped_gemm_int8", _ptr(xpq), _ptr(sxp), _ptr(counts), _ptr(offsets), _ptr(Wq), _ptr(sw), T, K, N, E, k,
@@ -607,10 +617,12 @@ def moe_permute_int8(topk_idx, xq, sx, E: int, ws: torch.Tensor, stream=None):
     _tensors(torch.int8, (xq, (T, d), "xq"))
     _tensors(torch.float32, (sx, (T,), "sx"))
     _tensors(torch.uint8, (ws, (ws.numel(),), "ws"))
-    i32 = torch.int32
-    # an empty batch enqueues no work: its counts are set here
-    counts, offsets = _empty(stream, ((E,), i32), ((E + 1,), i32), make=torch.empty if T else torch.zeros)
-    perm, inv, xpq, sxp = _empty(stream, ((P,), i32), ((P,), i32), ((P, d), torch.int8), ((P,), torch.float32))
+    counts, offsets = _new(stream, topk_idx, (E,)), _new(stream, topk_idx, (E + 1,))
+    perm, inv = _new(stream, topk_idx, (P,)), _new(stream, topk_idx, (P,))
+    xpq, sxp = _new(stream, xq, (P, d)), _new(stream, sx, (P,))
+    if T == 0:      # an empty batch enqueues no work of the library's
+        with torch.cuda.stream(stream):
+            counts.zero_(), offsets.zero_()
     _call("moe_permute_int8", _ptr(topk_idx), _ptr(xq), _ptr(sx), T, d, E, k, _ptr(counts), _ptr(offsets), _ptr(perm),
           _ptr(inv), _ptr(xpq), _ptr(sxp), _ptr(ws), ws.numel(), _queue(stream))
     return counts, offsets, perm, inv, xpq, sxp
@@ -628,7 +640,7 @@ def moe_combine_weighted(y_p, inv_perm, topk_w, shared_out=None, out=None, strea
     _tensors(torch.float32, (topk_w, (T, k), "topk_w"))
     _tensors(torch.int32, (inv_perm, (T * k,), "inv_perm"))
     if out is None:
-        (out,) = _empty(stream, ((T, d), torch.bfloat16))
+        out = _new(stream, y_p, (T, d))
     _call("moe_combine_weighted", _ptr(y_p), _ptr(inv_perm), _ptr(topk_w), _ptr(shared_out), T, k, d, _ptr(out),
           _queue(stream))
     return out
@@ -647,9 +659,9 @@ def moe_combine_weighted_backward(dout, y_p, inv_perm, topk_w, dy_p=None, dw=Non
     if dw is not None:
         _tensors(torch.float32, (dw, (T, k), "dw"))
     if dy_p is None:
-        (dy_p,) = _empty(stream, ((T * k, d), torch.bfloat16))
+        dy_p = _new(stream, y_p)
     if dw is None:
-        (dw,) = _empty(stream, ((T, k), torch.float32))
+        dw = _new(stream, topk_w)
     _call("moe_combine_weighted_backward", _ptr(dout), _ptr(y_p), _ptr(inv_perm), _ptr(topk_w), T, k, d, _ptr(dy_p),
           _ptr(dw), _queue(stream))
     return dy_p, dw
@@ -666,6 +678,6 @@ def moe_permute_backward(dxp, inv_perm, T: int, k: int, addend=None, dx=None, st
     _tensors(torch.bfloat16, *named)
     _tensors(torch.int32, (inv_perm, (T * k,), "inv_perm"))
     if dx is None:
-        (dx,) = _empty(stream, ((T, d), torch.bfloat16))
+        dx = _new(stream, dxp, (T, d))
     _call("moe_permute_backward", _ptr(dxp), _ptr(inv_perm), _ptr(addend), T, k, d, _ptr(dx), _queue(stream))
     return dx
