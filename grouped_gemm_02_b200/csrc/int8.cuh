@@ -267,30 +267,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     const int first = FORM == I8_SINGLE ? (int)blockIdx.x : (int)ptx::cluster_id_x();
     const int step = FORM == I8_SINGLE ? (int)gridDim.x : (int)ptx::nclusters_x();
 
-    ptx::grid_dep_wait();
-    ptx::grid_dep_launch();
-    constexpr int kRows = PAIR ? 256 : 128;
-    const int mt = (a.N + kRows - 1) / kRows;
-    const int nk = (a.K + kI8BlockK - 1) / kI8BlockK;
-    int total = a.units * mt, widest = min(a.chunk, a.T);
-    if (a.counts) {
-        if (!i8_plan(a, splan, mt, nk, step, PAIR)) {
-            // segments outside the rows: every CTA sees the same counts and leaves here
-            if (threadIdx.x == 0) atomicOr(a.err, DEVERR_PLAN);
-            return;
-        }
-        total = splan->tb[splan->nb] * mt;
-        widest = splan->widest;
-    }
-    const int n_max = PAIR ? max(32, (widest + 31) & ~31) : max(16, (widest + 15) & ~15);
-    const uint32_t stage_bytes = kATileBytes + (uint32_t)(PAIR ? n_max / 2 : n_max) * kBRowBytes;
-    const int stages = min(kMaxStages, (int)(kI8RingBytes / stage_bytes));
-    // I8_SPLIT: this CTA's K blocks (the host launches no more CTAs a tile than K blocks)
-    const int kb0 = FORM == I8_SPLIT ? (int)((int64_t)nk * rank / split) : 0;
-    const int kb1 = FORM == I8_SPLIT ? (int)((int64_t)nk * (rank + 1) / split) : nk;
-
+    // Barriers, descriptors and TMEM first: this part may run while the kernel before drains.
     if (threadIdx.x == 0) {
-        for (int s = 0; s < stages; s++) {
+        for (int s = 0; s < kMaxStages; s++) {
             ptx::mbar_init(ptx::smem_u32(&ctl->full[s]), 1);
             ptx::mbar_init(ptx::smem_u32(&ctl->empty[s]), 1);
         }
@@ -317,6 +296,26 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             ptx::tmem_relinquish();
         }
     }
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    constexpr int kRows = PAIR ? 256 : 128;
+    const int mt = (a.N + kRows - 1) / kRows;
+    const int nk = (a.K + kI8BlockK - 1) / kI8BlockK;
+    int total = a.units * mt, widest = min(a.chunk, a.T);
+    if (a.counts) {
+        const bool ok = i8_plan(a, splan, mt, nk, step, PAIR);
+        if (!ok && threadIdx.x == 0) atomicOr(a.err, DEVERR_PLAN);
+        // segments outside the rows: every CTA sees the same counts and takes no tile
+        total = ok ? splan->tb[splan->nb] * mt : 0;
+        widest = ok ? splan->widest : 32;
+    }
+    const int n_max = PAIR ? max(32, (widest + 31) & ~31) : max(16, (widest + 15) & ~15);
+    const uint32_t stage_bytes = kATileBytes + (uint32_t)(PAIR ? n_max / 2 : n_max) * kBRowBytes;
+    const int stages = min(kMaxStages, (int)(kI8RingBytes / stage_bytes));
+    // I8_SPLIT: this CTA's K blocks (the host launches no more CTAs a tile than K blocks)
+    const int kb0 = FORM == I8_SPLIT ? (int)((int64_t)nk * rank / split) : 0;
+    const int kb1 = FORM == I8_SPLIT ? (int)((int64_t)nk * (rank + 1) / split) : nk;
+
     ptx::tc_fence_before();
     if (PAIR) ptx::cluster_sync();
     else __syncthreads();

@@ -617,8 +617,8 @@ def moe_permute_int8(topk_idx, xq, sx, E: int, ws: torch.Tensor, stream=None):
     _tensors(torch.int8, (xq, (T, d), "xq"))
     _tensors(torch.float32, (sx, (T,), "sx"))
     _tensors(torch.uint8, (ws, (ws.numel(),), "ws"))
-    counts, offsets = _new(stream, topk_idx, (E,)), _new(stream, topk_idx, (E + 1,))
-    perm, inv = _new(stream, topk_idx, (P,)), _new(stream, topk_idx, (P,))
+    # one allocation for the four index arrays (each allocation costs the host about 2 us)
+    counts, offsets, perm, inv = _new(stream, topk_idx, (2 * E + 1 + 2 * P,)).split((E, E + 1, P, P))
     xpq, sxp = _new(stream, xq, (P, d)), _new(stream, sx, (P,))
     if T == 0:      # an empty batch enqueues no work of the library's
         with torch.cuda.stream(stream):
