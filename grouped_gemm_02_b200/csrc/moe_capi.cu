@@ -1628,11 +1628,16 @@ int moe_permute_int8(const int32_t* topk_idx, const int8_t* xq, const float* sx,
     if ((rc = device_setup(&dev))) return rc;
     cudaStream_t st = as_stream(stream);
     uint32_t* err = at<uint32_t>(ws, L.err);
-    if (T * k <= kSmallPairs) {
-        if (launch(permute_small_kernel, dim3(1), dim3(1024), 0, st, topk_idx, (int)(T * k), (int)E, counts, offsets,
-                   perm, inv_perm, (int32_t*)nullptr, 0, 0, 0, 0, kPlanSingle, err) != cudaSuccess)
-            return MOE_ERR_CUDA;
-    } else if (T * k <= kSortPairs) {
+    const uint8_t* xb = reinterpret_cast<const uint8_t*>(xq);
+    uint8_t* xpb = reinterpret_cast<uint8_t*>(xpq);
+    if (T * k <= kSortChunk) {
+        // a warp for each 512 bytes of a row, at most one CTA an SM
+        const int64_t items = T * ((d / 16 + 31) / 32);
+        return status_of(launch(sort_small_kernel, dim3((unsigned)std::min<int64_t>(items, dev->sm_count)),
+                                dim3(kSortChunk), 0, st, topk_idx, xb, sx, (int)T, (int)k, (int)d, (int)E, counts,
+                                offsets, perm, inv_perm, xpb, sxp, err));
+    }
+    if (T * k <= kSortPairs) {
         // chunks * E counts take the place of the logits: at most T * k / 512 * E < T * E of them
         const int P = (int)(T * k), chunks = sort_chunks(P);
         int32_t* hist = at<int32_t>(ws, L.logits);
@@ -1647,8 +1652,7 @@ int moe_permute_int8(const int32_t* topk_idx, const int8_t* xq, const float* sx,
         return rc;
     }
     return status_of(launch(gather_rows_int8_kernel, dim3(gather_blocks(T, (int)(d / 16), dev->sm_count)), dim3(256),
-                            0, st, reinterpret_cast<const uint8_t*>(xq), sx, (const int32_t*)inv_perm, T, (int)k,
-                            (int)d, reinterpret_cast<uint8_t*>(xpq), sxp));
+                            0, st, xb, sx, (const int32_t*)inv_perm, T, (int)k, (int)d, xpb, sxp));
 }
 
 // Sizes of the entry points that only read a permutation.

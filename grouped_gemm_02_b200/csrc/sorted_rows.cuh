@@ -128,8 +128,24 @@ __global__ void __launch_bounds__(kSortChunk) chunk_rank_kernel(const int32_t* _
 }
 
 // ---------------------------------------------------------------- sort: int8 rows with a scale each
-// One warp per (token, 512-byte chunk of the row): a 16-byte vector per lane,
-// then its k stores; the first chunk's warp also writes the scales.
+// Copies chunk c of token t's row (512 bytes: a 16-byte vector a lane) to its
+// pairs' positions; the first chunk's warp also writes the scales.  `mine`: the
+// position of pair t k + lane, or -1.
+__device__ __forceinline__ void copy_row_chunk(const uint8_t* __restrict__ xq, const float* __restrict__ sx, int64_t t,
+                                               int c, int mine, int k, int d, uint8_t* __restrict__ xpq,
+                                               float* __restrict__ sxp)
+{
+    const int v = c * 32 + (int)(threadIdx.x & 31), nvec = d / 16;
+    uint4 buf = make_uint4(0u, 0u, 0u, 0u);
+    if (v < nvec) buf = __ldg(reinterpret_cast<const uint4*>(xq + t * d) + v);
+    if (c == 0 && mine >= 0) sxp[mine] = sx[t];
+    for (int j = 0; j < k; j++) {
+        const int pos = __shfl_sync(0xffffffffu, mine, j);
+        if (pos >= 0 && v < nvec) reinterpret_cast<uint4*>(xpq + (int64_t)pos * d)[v] = buf;
+    }
+}
+
+// One warp per (token, chunk).
 __global__ void __launch_bounds__(256) gather_rows_int8_kernel(const uint8_t* __restrict__ xq,
                                                                const float* __restrict__ sx,
                                                                const int32_t* __restrict__ inv_perm, int64_t T, int k,
@@ -138,22 +154,79 @@ __global__ void __launch_bounds__(256) gather_rows_int8_kernel(const uint8_t* __
 {
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    const int nvec = d / 16, nch = (nvec + 31) / 32;
+    const int nch = (d / 16 + 31) / 32;
     const int lane = threadIdx.x & 31;
     const int64_t items = T * nch, P = T * k;
     for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 32; w < items;
          w += (int64_t)gridDim.x * blockDim.x / 32) {
         const int64_t t = w / nch;
-        const int c = (int)(w - t * nch);
-        const int v = c * 32 + lane;
         const int mine = lane < k ? pair_pos(inv_perm, t * k + lane, P) : -1;
-        uint4 buf = make_uint4(0u, 0u, 0u, 0u);
-        if (v < nvec) buf = __ldg(reinterpret_cast<const uint4*>(xq + t * d) + v);
-        if (c == 0 && mine >= 0) sxp[mine] = sx[t];
-        for (int j = 0; j < k; j++) {
-            const int pos = __shfl_sync(0xffffffffu, mine, j);
-            if (pos >= 0 && v < nvec) reinterpret_cast<uint4*>(xpq + (int64_t)pos * d)[v] = buf;
+        copy_row_chunk(xq, sx, t, (int)(w - t * nch), mine, k, d, xpq, sxp);
+    }
+}
+
+// At most 1024 pairs (one a thread): the whole sort in one launch.  Every CTA
+// finds all positions for itself -- a second launch would cost more than the
+// repeated ranking -- and copies its share of the rows; CTA 0 also writes the
+// index arrays and reports bad expert ids.
+__global__ void __launch_bounds__(kSortChunk) sort_small_kernel(const int32_t* __restrict__ idx,
+                                                                const uint8_t* __restrict__ xq,
+                                                                const float* __restrict__ sx, int T, int k, int d,
+                                                                int E, int32_t* __restrict__ counts,
+                                                                int32_t* __restrict__ offsets,
+                                                                int32_t* __restrict__ perm,
+                                                                int32_t* __restrict__ inv_perm,
+                                                                uint8_t* __restrict__ xpq, float* __restrict__ sxp,
+                                                                uint32_t* __restrict__ err)
+{
+    __shared__ __align__(16) uint8_t s_wcnt[32][kMaxExperts];   // pairs of a warp (at most 32) by expert
+    __shared__ int s_off[kMaxExperts];
+    __shared__ int s_pos[kSortChunk];
+    __shared__ int warp_sums[32];
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int P = T * k;
+    const bool first = blockIdx.x == 0;
+    int e = tid < P ? idx[tid] : -1;
+    const bool bad = tid < P && (e < 0 || e >= E);
+    if (bad) e = -1;
+    if (bad && first) atomicOr(err, DEVERR_EXPERT_RANGE);
+    reinterpret_cast<uint4*>(&s_wcnt[0][0])[tid] = make_uint4(0, 0, 0, 0);   // 1024 x 16 B = the whole table
+    __syncthreads();
+    const unsigned peers = __match_any_sync(0xffffffffu, e);
+    const int rank = __popc(peers & ((1u << lane) - 1u));
+    if (e >= 0 && lane == __ffs(peers) - 1) s_wcnt[warp][e] = (uint8_t)__popc(peers);
+    __syncthreads();
+    const int warps = (P + 31) / 32;
+    int total = 0;
+    if (tid < E)
+        for (int w = 0; w < warps; w++) total += s_wcnt[w][tid];
+    const int incl = block_inclusive_scan(total, warp_sums);
+    if (tid < E) {
+        s_off[tid] = incl - total;
+        if (first) {
+            counts[tid] = total;
+            offsets[tid] = incl - total;
+            if (tid == E - 1) offsets[E] = incl;
         }
+    }
+    __syncthreads();
+    int pos = -1;
+    if (e >= 0) {
+        pos = s_off[e] + rank;
+        for (int w = 0; w < warp; w++) pos += s_wcnt[w][e];
+        if (first) perm[pos] = tid;
+    }
+    s_pos[tid] = pos;
+    if (first && tid < P) inv_perm[tid] = pos;
+    __syncthreads();
+    const int nch = (d / 16 + 31) / 32, items = T * nch;
+    // dealt over the CTAs first: few rows are then written by many SMs
+    for (int w = warp * gridDim.x + blockIdx.x; w < items; w += gridDim.x * 32) {
+        const int t = w / nch;
+        const int mine = lane < k ? s_pos[t * k + lane] : -1;
+        copy_row_chunk(xq, sx, t, w - t * nch, mine, k, d, xpq, sxp);
     }
 }
 

@@ -9,6 +9,7 @@ device is not a B200, the call raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 from typing import Optional
@@ -454,16 +455,15 @@ def _check_stream(stream) -> None:
     _need(stream.device_index == dev, f"stream: expected one of cuda:{dev}, got one of {stream.device}")
 
 
-def _new(stream, like: torch.Tensor, shape=None, dtype=None) -> torch.Tensor:
-    """A new tensor on the device of ``like`` (which has been checked), owned by the stream that will write it;
-    of its shape and dtype where none is given."""
-    if stream is not None:
-        _check_stream(stream)
-        with torch.cuda.stream(stream):
-            return _new(None, like, shape, dtype)
-    if shape is None:
-        return torch.empty_like(like, dtype=dtype)
-    return like.new_empty(shape, dtype=dtype)
+def _on(stream):
+    """The context in which a call's new tensors are made: they belong to the stream that will write them."""
+    if stream is None:
+        return _HERE
+    _check_stream(stream)
+    return torch.cuda.stream(stream)
+
+
+_HERE = contextlib.nullcontext()
 
 
 # The handle of the current stream of a device, without the Python object around it (0.1 us instead of 3).
@@ -484,7 +484,7 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _norm_args(x, weight, residual, xsum, y, stream):
+def _norm_args(x, weight, residual, xsum, y):
     T, d = rows = _rows_of(x, "x")
     named = [(x, rows, "x"), (weight, (d,), "weight")]
     if residual is not None:
@@ -496,16 +496,17 @@ def _norm_args(x, weight, residual, xsum, y, stream):
     if y is not None:
         named.append((y, rows, "y"))
     _tensors(torch.bfloat16, *named)
-    if residual is not None and xsum is None:
-        xsum = _new(stream, x)
-    return T, d, xsum
+    return T, d
 
 
 def moe_rmsnorm(x, weight, eps: float, residual=None, xsum=None, y=None, stream=None):
     """y = rmsnorm(x) * weight; with a residual, (rmsnorm(x + residual) * weight, x + residual)."""
-    T, d, xsum = _norm_args(x, weight, residual, xsum, y, stream)
-    if y is None:
-        y = _new(stream, x)
+    T, d = _norm_args(x, weight, residual, xsum, y)
+    with _on(stream):
+        if xsum is None and residual is not None:
+            xsum = torch.empty_like(x)
+        if y is None:
+            y = torch.empty_like(x)
     _call("moe_rmsnorm", _ptr(x), _ptr(residual), _ptr(weight), T, d, eps, _ptr(xsum), _ptr(y), _queue(stream))
     return y if residual is None else (y, xsum)
 
@@ -513,8 +514,11 @@ def moe_rmsnorm(x, weight, eps: float, residual=None, xsum=None, y=None, stream=
 def moe_rmsnorm_fp8(x, weight, eps: float, residual=None, xsum=None, y=None, stream=None):
     """moe_rmsnorm with e4m3 codes and 1 x 128 scales: (q, scales) or, with a residual, (q, scales, xsum).
     ``y`` (optional, given by the caller) also receives the bf16 result."""
-    T, d, xsum = _norm_args(x, weight, residual, xsum, y, stream)
-    q, sc = _new(stream, x, dtype=torch.uint8), _new(stream, x, (T, d // 128), torch.float32)
+    T, d = _norm_args(x, weight, residual, xsum, y)
+    with _on(stream):
+        if xsum is None and residual is not None:
+            xsum = torch.empty_like(x)
+        q, sc = torch.empty_like(x, dtype=torch.uint8), x.new_empty((T, d // 128), dtype=torch.float32)
     _call("moe_rmsnorm_fp8", _ptr(x), _ptr(residual), _ptr(weight), T, d, eps, _ptr(xsum), _ptr(y), _ptr(q), _ptr(sc),
           _queue(stream))
     return (q, sc) if residual is None else (q, sc, xsum)
@@ -523,8 +527,11 @@ def moe_rmsnorm_fp8(x, weight, eps: float, residual=None, xsum=None, y=None, str
 def moe_rmsnorm_int8(x, weight, eps: float, residual=None, xsum=None, y=None, stream=None):
     """moe_rmsnorm with int8 codes and one scale a row: (q, scale) or, with a residual, (q, scale, xsum).
     ``y`` (optional, given by the caller) also receives the bf16 result."""
-    T, d, xsum = _norm_args(x, weight, residual, xsum, y, stream)
-    q, sc = _new(stream, x, dtype=torch.int8), _new(stream, x, (T,), torch.float32)
+    T, d = _norm_args(x, weight, residual, xsum, y)
+    with _on(stream):
+        if xsum is None and residual is not None:
+            xsum = torch.empty_like(x)
+        q, sc = torch.empty_like(x, dtype=torch.int8), x.new_empty(T, dtype=torch.float32)
     _call("moe_rmsnorm_int8", _ptr(x), _ptr(residual), _ptr(weight), T, d, eps, _ptr(xsum), _ptr(y), _ptr(q), _ptr(sc),
           _queue(stream))
     return (q, sc) if residual is None else (q, sc, xsum)
@@ -551,12 +558,13 @@ def moe_rmsnorm_backward(dy, xsum, weight, eps: float, dxsum=None, dx=None, dwei
         _tensors(torch.float32, (dweight, (d,), "dweight"))
     if ws is not None:
         _tensors(torch.uint8, (ws, (ws.numel(),), "ws"))
-    if dx is None:
-        dx = _new(stream, dy)
-    if dweight is None:
-        dweight = _new(stream, dy, (d,), torch.float32)
-    if ws is None:
-        ws = _new(stream, dy, (moe_rmsnorm_backward_workspace_size(T, d),), torch.uint8)
+    with _on(stream):
+        if dx is None:
+            dx = torch.empty_like(dy)
+        if dweight is None:
+            dweight = dy.new_empty(d, dtype=torch.float32)
+        if ws is None:
+            ws = dy.new_empty(moe_rmsnorm_backward_workspace_size(T, d), dtype=torch.uint8)
     _call("moe_rmsnorm_backward", _ptr(dy), _ptr(xsum), _ptr(weight), _ptr(dxsum), T, d, eps, _ptr(dx), _ptr(dweight),
           _ptr(ws), ws.numel(), _queue(stream))
     return dx, dweight
@@ -568,7 +576,8 @@ def moe_quantize_int8_rows(x: torch.Tensor, stream=None):
     _tensors(torch.bfloat16, (x, x.shape, "x"))
     Cc = x.shape[-1]
     R = x.numel() // Cc if Cc else 0
-    q, sc = _new(stream, x, dtype=torch.int8), _new(stream, x, x.shape[:-1], torch.float32)
+    with _on(stream):
+        q, sc = torch.empty_like(x, dtype=torch.int8), x.new_empty(x.shape[:-1], dtype=torch.float32)
     _call("moe_quantize_int8_rows", _ptr(x), R, Cc, _ptr(q), _ptr(sc), _queue(stream))
     return q, sc
 
@@ -580,7 +589,8 @@ def moe_gemm_int8(xq, sx, Wq, sw, ws: torch.Tensor, out=None, stream=None):
     _tensors(torch.float32, (sx, (T,), "sx"), (sw, (N,), "sw"))
     _tensors(torch.uint8, (ws, (ws.numel(),), "ws"))
     if out is None:
-        out = _new(stream, xq, (T, N), torch.bfloat16)
+        with _on(stream):
+            out = xq.new_empty((T, N), dtype=torch.bfloat16)
     else:
         _tensors(torch.bfloat16, (out, (T, N), "out"))
     _call("moe_gemm_int8", _ptr(xq), _ptr(sx), _ptr(Wq), _ptr(sw), T, K, N, _ptr(out), _ptr(ws), ws.numel(),
@@ -600,7 +610,8 @@ def moe_grouped_gemm_int8(xpq, sxp, counts, offsets, Wq, sw, T: int, k: int, ws:
     _tensors(torch.int32, (counts, (E,), "counts"), (offsets, (E + 1,), "offsets"))
     _tensors(torch.uint8, (ws, (ws.numel(),), "ws"))
     if out is None:
-        out = _new(stream, xpq, (P, N), torch.bfloat16)
+        with _on(stream):
+            out = xpq.new_empty((P, N), dtype=torch.bfloat16)
     else:
         _tensors(torch.bfloat16, (out, (P, N), "out"))
     _call("moe_grouped_gemm_int8", _ptr(xpq), _ptr(sxp), _ptr(counts), _ptr(offsets), _ptr(Wq), _ptr(sw), T, K, N, E, k,
@@ -617,11 +628,10 @@ def moe_permute_int8(topk_idx, xq, sx, E: int, ws: torch.Tensor, stream=None):
     _tensors(torch.int8, (xq, (T, d), "xq"))
     _tensors(torch.float32, (sx, (T,), "sx"))
     _tensors(torch.uint8, (ws, (ws.numel(),), "ws"))
-    # one allocation for the four index arrays (each allocation costs the host about 2 us)
-    counts, offsets, perm, inv = _new(stream, topk_idx, (2 * E + 1 + 2 * P,)).split((E, E + 1, P, P))
-    xpq, sxp = _new(stream, xq, (P, d)), _new(stream, sx, (P,))
-    if T == 0:      # an empty batch enqueues no work of the library's
-        with torch.cuda.stream(stream):
+    with _on(stream):
+        counts, offsets, perm, inv = (topk_idx.new_empty(n) for n in (E, E + 1, P, P))
+        xpq, sxp = xq.new_empty((P, d)), sx.new_empty(P)
+        if T == 0:      # an empty batch enqueues no work of the library's
             counts.zero_(), offsets.zero_()
     _call("moe_permute_int8", _ptr(topk_idx), _ptr(xq), _ptr(sx), T, d, E, k, _ptr(counts), _ptr(offsets), _ptr(perm),
           _ptr(inv), _ptr(xpq), _ptr(sxp), _ptr(ws), ws.numel(), _queue(stream))
@@ -640,7 +650,8 @@ def moe_combine_weighted(y_p, inv_perm, topk_w, shared_out=None, out=None, strea
     _tensors(torch.float32, (topk_w, (T, k), "topk_w"))
     _tensors(torch.int32, (inv_perm, (T * k,), "inv_perm"))
     if out is None:
-        out = _new(stream, y_p, (T, d))
+        with _on(stream):
+            out = y_p.new_empty((T, d))
     _call("moe_combine_weighted", _ptr(y_p), _ptr(inv_perm), _ptr(topk_w), _ptr(shared_out), T, k, d, _ptr(out),
           _queue(stream))
     return out
@@ -658,10 +669,11 @@ def moe_combine_weighted_backward(dout, y_p, inv_perm, topk_w, dy_p=None, dw=Non
     _tensors(torch.int32, (inv_perm, (T * k,), "inv_perm"))
     if dw is not None:
         _tensors(torch.float32, (dw, (T, k), "dw"))
-    if dy_p is None:
-        dy_p = _new(stream, y_p)
-    if dw is None:
-        dw = _new(stream, topk_w)
+    with _on(stream):
+        if dy_p is None:
+            dy_p = torch.empty_like(y_p)
+        if dw is None:
+            dw = torch.empty_like(topk_w)
     _call("moe_combine_weighted_backward", _ptr(dout), _ptr(y_p), _ptr(inv_perm), _ptr(topk_w), T, k, d, _ptr(dy_p),
           _ptr(dw), _queue(stream))
     return dy_p, dw
@@ -678,6 +690,7 @@ def moe_permute_backward(dxp, inv_perm, T: int, k: int, addend=None, dx=None, st
     _tensors(torch.bfloat16, *named)
     _tensors(torch.int32, (inv_perm, (T * k,), "inv_perm"))
     if dx is None:
-        dx = _new(stream, dxp, (T, d))
+        with _on(stream):
+            dx = dxp.new_empty((T, d))
     _call("moe_permute_backward", _ptr(dxp), _ptr(inv_perm), _ptr(addend), T, k, d, _ptr(dx), _queue(stream))
     return dx
