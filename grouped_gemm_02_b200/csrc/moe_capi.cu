@@ -1376,25 +1376,27 @@ extern "C" int moe_permute_noalloc(const int32_t* topk_idx, const moe_bf16* x, i
 // ---------------------------------------------------------------- norms, int8 products, sorted rows
 namespace {
 
-// Warps of a row and rows of a CTA for a forward row kernel.  Few rows: one vector a
-// thread, the shortest path from load to store; from two rows an SM on: four
-// vectors a thread (two took 171 us against 137 at T=16384 d=7168 e4m3), but no more
-// than one warp's share of the row (T=16384 d=512: 11.9 us with two, 15.0 with four).
+// Warps of a row and rows of a CTA for a forward row kernel.  Few rows: 16 values a
+// thread, the shortest path from load to store; from two rows an SM on: 32 values a
+// thread, more bytes in flight and fewer warps to join (16 took 171 us against 137 at
+// T=16384 d=7168 e4m3), unless a warp's 16 a lane hold the row.
 RowShape norm_shape(int64_t T, int d, int sms)
 {
-    const int nvec = d / 8;
-    int vpt = T >= 2 * (int64_t)sms ? 4 : 1;
-    while (vpt > 1 && nvec <= 16 * vpt) vpt /= 2;
-    while (row_warps(nvec, vpt) > 32) vpt *= 2;
-    return row_shape(nvec, vpt);
+    const int nw = d / 16;
+    int wpt = T >= 2 * (int64_t)sms && nw > 32 ? 2 : 1;
+    while (row_warps(nw, wpt) > 32) wpt *= 2;
+    return row_shape(nw, wpt);
 }
 
+inline bool al32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 template <int OUT>
-int run_norm(const NormArgs& a, int sms, cudaStream_t st)
+int run_norm(NormArgs a, int sms, cudaStream_t st)
 {
+    a.al32 = al32(a.x) && al32(a.residual) && al32(a.weight) && al32(a.xsum) && al32(a.y);
     const RowShape s = norm_shape(a.T, a.d, sms);
     const dim3 grid((unsigned)((a.T + s.groups - 1) / s.groups)), block(s.warps * s.groups * 32);
-    auto kernel = s.vpt == 1 ? rmsnorm_kernel<OUT, 1> : s.vpt == 2 ? rmsnorm_kernel<OUT, 2> : rmsnorm_kernel<OUT, 4>;
+    auto kernel = s.vpt == 1 ? rmsnorm_kernel<OUT, 1> : rmsnorm_kernel<OUT, 2>;
     return status_of(launch(kernel, grid, block, 0, st, a, s.warps));
 }
 
@@ -1433,6 +1435,7 @@ int norm_entry(const moe_bf16* x, const moe_bf16* residual, const moe_bf16* weig
     a.T = T;
     a.d = (int)d;
     a.eps = eps;
+    a.inv_d = 1.0 / (double)d;
     return run_norm<OUT>(a, dev->sm_count, as_stream(stream));
 }
 

@@ -1,9 +1,10 @@
 """Residual addition with root-mean-square norm, its gradient and the int8 row quantiser on the GPU against
 their 64-bit definitions (marked gpu).
 
-Tolerances, each result rounded to bf16 once (half a step, 2^-8 relative).  Before that, fp32: the mean of
-squares adds at most 8 * 4 values a thread and 10 levels of a tree, so its relative error is below 64 * 2^-24;
-rsqrt halves it and adds 2 ulp, and two products follow: below 2^-18 in all, written as 2^-17."""
+Tolerances, each result rounded to bf16 once (half a step, 2^-8 relative).  Before that, fp32: in the gradient the
+mean of squares adds at most 8 * 4 values a thread and 10 levels of a tree, so its relative error is below 64 * 2^-24;
+rsqrt halves it and adds 2 ulp, and two products follow: below 2^-18 in all, written as 2^-17.  The forward pass
+stays within that too."""
 
 from __future__ import annotations
 
@@ -192,6 +193,32 @@ def test_norm_in_place():
         a, b = dy.clone(), ds.clone()
         dx1, dw1 = moe.moe_rmsnorm_backward(a, s, w, EPS, dxsum=b, dx=a if buf == "dy" else b)
         assert torch.equal(dx1, dx) and torch.equal(dw1, dw)
+
+
+@pytest.mark.parametrize("d", [128, 1152, 7168])
+def test_norm_of_tensors_aligned_to_16_bytes_only(d):
+    """The documented alignment is 16 bytes: views that start there give what aligned copies give."""
+    T = 9
+    def view(t):
+        buf = torch.empty(t.numel() + 8, dtype=t.dtype, device=DEV)[8:].view(t.shape)
+        assert buf.data_ptr() % 32 == 16
+        return buf.copy_(t)
+    x, r, w = _rows(T, d, 40), _rows(T, d, 41), _weight(d, 42)
+    y, s = moe.moe_rmsnorm(x.to(DEV), w.to(DEV), EPS, residual=r.to(DEV))
+    ov = view(torch.zeros(T, d, dtype=torch.bfloat16))
+    y1, s1 = moe.moe_rmsnorm(view(x), view(w), EPS, residual=view(r), xsum=ov)
+    assert torch.equal(y, y1) and torch.equal(s, s1)
+    for f in (moe.moe_rmsnorm_fp8, moe.moe_rmsnorm_int8):
+        a = f(x.to(DEV), w.to(DEV), EPS, residual=r.to(DEV))
+        b = f(view(x), view(w), EPS, residual=view(r), y=view(x))
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+    q, sc = moe.moe_quantize_int8_rows(view(x))
+    q1, sc1 = moe.moe_quantize_int8_rows(x.to(DEV))
+    assert torch.equal(q, q1) and torch.equal(sc, sc1)
+    dy, ds = R.randn(43, T, d), R.randn(44, T, d)
+    g = moe.moe_rmsnorm_backward(dy.to(DEV), s, w.to(DEV), EPS, dxsum=ds.to(DEV))
+    g1 = moe.moe_rmsnorm_backward(view(dy), view(s.cpu()), view(w), EPS, dxsum=view(ds), dx=view(dy))
+    assert torch.equal(g[0], g1[0]) and torch.equal(g[1], g1[1])
 
 
 def test_norm_refuses_what_it_cannot_take():
