@@ -74,9 +74,12 @@ inline Int8Shape i8_shape(int64_t T, int64_t K, int64_t N, int sms, bool can_pai
 }
 
 // Whether a grouped product of P rows over E experts runs on CTA pairs.  The host
-// knows the mean segment only; the rows of a tile are chosen on the device.
-// Measured on 64 experts, K = N = 2048: pairs 3 to 11% faster from 128 rows an
-// expert on, 5 to 7% slower at 16 and below.
+// knows the mean segment only; the rows of a tile are chosen on the device.  Pairs
+// run where they are at least a fifth cheaper by i8_cost and the experts' weights,
+// at 6500 bytes/ns, do not take longer than the single CTAs' work.  Measured on
+// K = N = 2048, single CTAs against pairs: 64 experts with 4 rows each 42.5 and
+// 44.2 us, 128 rows 67 and 67, 256 rows 95 and 87, 512 rows 166 and 154; 16
+// experts with 512 rows at K = N = 1024 20.8 and 23.2 (the estimate: 4% cheaper).
 inline bool i8_grouped_pair(int64_t P, int64_t K, int64_t N, int64_t E, int sms, bool can_pair, int pairs)
 {
     if (!can_pair) return false;
@@ -85,7 +88,8 @@ inline bool i8_grouped_pair(int64_t P, int64_t K, int64_t N, int64_t E, int sms,
     const int chunk = rows >= 256 ? 256 : (int)((rows + 31) / 32 * 32);
     // the mean segments end to end, as one dense product of whole tiles
     const int64_t T = blocks * ((rows + chunk - 1) / chunk) * chunk;
-    return i8_cost(T, K, N, sms, I8_PAIR, chunk, 1) < i8_cost(T, K, N, sms, I8_SINGLE, chunk, 1);
+    const double single = i8_cost(T, K, N, sms, I8_SINGLE, chunk, 1), pair = i8_cost(T, K, N, sms, I8_PAIR, chunk, 1);
+    return pair < 0.8 * single && (double)blocks * (double)N * (double)K / 6500.0 < single;
 }
 
 }  // namespace moe

@@ -335,7 +335,8 @@ MOE_API int moe_grouped_gemm_int8(const int8_t *xpq, const float *sxp, const int
 /* moe_permute for int8 rows with a scale each: xq [T,d], sx [T] -> xpq [T*k,d],
  * sxp [T*k]; the other outputs, their order and the treatment of bad expert ids
  * are moe_permute's.  `ws` is a workspace of moe_workspace_size(T, d, f, E, k, 0)
- * bytes for any d and f; the layer's intermediates in it are not kept. */
+ * bytes for any d and f; the layer's intermediates in it are not kept, and two
+ * calls that may overlap need two. */
 MOE_API int moe_permute_int8(const int32_t *topk_idx, const int8_t *xq, const float *sx, int64_t T, int64_t d,
                              int64_t E, int64_t k, int32_t *counts, int32_t *offsets, int32_t *perm,
                              int32_t *inv_perm, int8_t *xpq, float *sxp, void *ws, size_t ws_bytes, void *stream);
@@ -381,7 +382,8 @@ MOE_API int moe_record_phase_events(void *const *events, int n);
  *                          (cta_group::2), 0: single-CTA tiles of 128 rows
  *                          (rule: the bf16 GEMMs take pairs whenever two
  *                          launches run; the FP8 / FP4 GEMMs take them only
- *                          when this is 1 and two launches run)
+ *                          when this is 1 and two launches run; the int8
+ *                          products by their sizes)
  *   MOE_POLICY_TILES       0 (rule): histogram-matched tiles -- the plan step
  *                          classifies the live histogram on the device (tokens
  *                          per effective expert, hottest expert against that

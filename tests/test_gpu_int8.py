@@ -43,6 +43,56 @@ def test_gemm_int8(T, K, N):
     assert (out[T:] == 7.0).all()
 
 
+@pytest.fixture
+def pairs(request):
+    moe.moe_set_policy(moe.POLICY_CTA_PAIRS, request.param)
+    yield request.param
+    moe.moe_set_policy(moe.POLICY_CTA_PAIRS, -1)
+
+
+@pytest.mark.parametrize("pairs", [0, 1], indirect=True)
+@pytest.mark.parametrize("T,K,N", [(1, 64, 64), (16, 128, 128), (17, 4096, 1088), (33, 2048, 320), (257, 640, 640),
+                                   (1000, 2048, 1024), (300, 2048, 19200)])
+def test_gemm_int8_every_form(pairs, T, K, N):
+    """Integer sums: single CTAs, CTA pairs and shared K ranges give the same bits."""
+    xq, sx, wq, sw = (t.to(DEV) for t in _dense(T, K, N, seed=T + N))
+    got = moe.moe_gemm_int8(xq, sx, wq, sw, _ws(T))
+    moe.moe_set_policy(moe.POLICY_CTA_PAIRS, -1)
+    rule = moe.moe_gemm_int8(xq, sx, wq, sw, _ws(T))
+    assert torch.equal(got, rule)
+    ref = R.int8_gemm(xq, sx, wq, sw)
+    R.within(got, ref, REL * ref.abs() + R.TINY, f"pairs={pairs} T={T} K={K} N={N}")
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 7168, 7168), (1, 7168, 4096), (3, 16384, 512)])
+def test_gemm_int8_shared_k_ranges_rerun(T, K, N):
+    """Two, four and eight CTAs a tile: the same bits in every run, and with no rows or channels lost."""
+    xq, sx, wq, sw = (t.to(DEV) for t in _dense(T, K, N, seed=N))
+    a, b = (moe.moe_gemm_int8(xq, sx, wq, sw, _ws(T)) for _ in range(2))
+    assert torch.equal(a, b)
+    ref = R.int8_gemm(xq, sx, wq, sw)
+    R.within(a, ref, REL * ref.abs() + R.TINY, f"T={T} K={K} N={N}")
+
+
+def test_gemm_int8_past_32_bit_offsets():
+    """Codes and results whose offsets pass 2^31: the last rows, where an overflow would show."""
+    T, K, N = 300_000, 64, 7232                         # T * N = 2.17e9 results
+    xq, sx = R.codes(5, T, K).to(DEV), R.scales(6, T).to(DEV)
+    wq, sw = R.codes(7, N, K).to(DEV), R.scales(8, N, mean=0.001).to(DEV)
+    out = moe.moe_gemm_int8(xq, sx, wq, sw, _ws(1))
+    for a in (0, T // 2, T - 300):
+        ref = R.int8_gemm(xq[a:a + 300], sx[a:a + 300], wq, sw)
+        R.within(out[a:a + 300], ref, REL * ref.abs() + R.TINY, f"rows {a}..")
+    del out
+    T, K, N = 40_000, 57_344, 64                        # T * K = 2.29e9 codes
+    xq = torch.randint(-127, 128, (T, K), dtype=torch.int8, device=DEV)
+    sx, wq, sw = R.scales(9, T).to(DEV), R.codes(10, N, K).to(DEV), R.scales(11, N, mean=1e-4).to(DEV)
+    out = moe.moe_gemm_int8(xq, sx, wq, sw, _ws(1))
+    for a in (0, T - 200):
+        ref = R.int8_gemm(xq[a:a + 200], sx[a:a + 200], wq, sw)
+        R.within(out[a:a + 200], ref, REL * ref.abs() + R.TINY, f"rows {a}..")
+
+
 @pytest.mark.parametrize("T,K,N", [(1, 65536, 64), (5, 65536, 192), (300, 65536, 2304)])
 def test_gemm_int8_extreme_sums(T, K, N):
     """Every code at its extreme, -128 included: sums of 2^30 stay exact."""
@@ -126,6 +176,19 @@ def _grouped_check(counts, T, k, K, N, seed):
 ])
 def test_grouped_gemm_int8(counts, T, k, K, N):
     _grouped_check(counts, T, k, K, N, seed=len(counts) + K)
+
+
+@pytest.mark.parametrize("pairs", [0, 1], indirect=True)
+@pytest.mark.parametrize("counts,T,k,K,N", [
+    ([0, 1, 0, 0], 1, 1, 2048, 192),
+    ([3, 0, 17, 1, 0, 16, 32, 5], 40, 2, 448, 704),
+    ([256, 257, 255, 1], 769, 1, 256, 320),
+    ([512, 511, 513, 500, 12, 0, 700, 1300], 506, 8, 2048, 1024),
+    ([0] * 511 + [7], 7, 1, 128, 64),
+    ([2] * 512, 1024, 1, 128, 64),
+])
+def test_grouped_gemm_int8_every_form(pairs, counts, T, k, K, N):
+    _grouped_check(counts, T, k, K, N, seed=K + N)
 
 
 @pytest.mark.parametrize("T,E,k,alpha,K,N", [(32, 64, 8, 1.0, 2048, 1024), (3, 512, 8, 0.1, 256, 128),

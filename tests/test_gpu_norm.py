@@ -176,6 +176,27 @@ def test_rmsnorm_backward_of_no_rows_and_reruns():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_norm_past_32_bit_offsets():
+    """Rows whose offsets pass 2^31 elements: the last rows, where an overflow would show."""
+    T, d = 300_100, 7168                                    # 2.15e9 elements
+    x = torch.empty(T, d, dtype=torch.bfloat16, device=DEV)
+    part = _rows(100, d, 50).to(DEV)
+    x[-100:] = part
+    x[:-100] = 1.0
+    w = _weight(d, 51).to(DEV)
+    q, sc = moe.moe_rmsnorm_int8(x, w, EPS)
+    q1, sc1 = moe.moe_rmsnorm_int8(part, w, EPS)
+    assert torch.equal(q[-100:], q1) and torch.equal(sc[-100:], sc1)
+    del q
+    dy = torch.zeros_like(x)
+    dy[-100:] = R.randn(52, 100, d).to(DEV)
+    dx, dw = moe.moe_rmsnorm_backward(dy, x, w, EPS)
+    rx, rw, mx, mw = R.rmsnorm_grad(dy[-100:], part, w, EPS)
+    R.within(dx[-100:], rx, R.BF16 * rx.abs() + NORM32 * mx + R.TINY, "dx")
+    R.within(dw, rw, (NORM32 + 400 * R.F32) * mw + R.TINY, "dweight")
+    assert (dx[:-100] == 0).all()
+
+
 def test_norm_in_place():
     """The buffers that the documentation allows to coincide."""
     T, d = 33, 1088

@@ -52,6 +52,60 @@ def test_permute_int8(T, E, k, d, drop):
     assert torch.equal(g[4][:n], xq[tok]) and torch.equal(g[5][:n], sx[tok])
 
 
+@pytest.mark.parametrize("T", [32768, 32769, 45000])
+def test_permute_int8_of_many_pairs(T):
+    """Around 2^18 pairs, where another way of finding the positions takes over."""
+    E, k, d = 24, 8, 64
+    idx = torch.randint(0, E, (T, k), generator=R.gen(T), dtype=torch.int32)
+    idx[5, 3], idx[T - 1, 7] = E, -2
+    xq, sx = R.codes(20, T, d), R.scales(21, T)
+    ws = moe.new_workspace(T, 64, 64, E, k)
+    got = [t.cpu() for t in moe.moe_permute_int8(idx.to(DEV), xq.to(DEV), sx.to(DEV), E, ws)]
+    assert moe.moe_get_device_error(ws) == moe.DEVERR_EXPERT_RANGE
+    flat = idx.reshape(-1).long()
+    ok = (flat >= 0) & (flat < E)
+    key, perm = torch.sort(torch.where(ok, flat, torch.full_like(flat, E)), stable=True)
+    n = int(ok.sum())
+    perm = perm[:n]
+    counts = torch.bincount(key[:n], minlength=E)
+    assert torch.equal(got[0].long(), counts) and torch.equal(got[1].long(), torch.cat([counts.new_zeros(1), counts.cumsum(0)]))
+    inv = torch.full((T * k,), -1, dtype=torch.int64)
+    inv[perm] = torch.arange(n)
+    assert torch.equal(got[2][:n].long(), perm) and torch.equal(got[3].long(), inv)
+    assert torch.equal(got[4][:n], xq[perm // k]) and torch.equal(got[5][:n], sx[perm // k])
+
+
+def test_sorted_rows_past_32_bit_offsets():
+    """Rows whose offsets pass 2^31 elements: the last positions, where an overflow would show."""
+    T, E, k, d = 40_000, 8, 8, 7168                          # T * k * d = 2.29e9
+    idx = torch.stack([torch.arange(E, dtype=torch.int32)] * T)
+    xq = torch.randint(-127, 128, (T, d), dtype=torch.int8, device=DEV)
+    sx = R.scales(22, T).to(DEV)
+    ws = moe.new_workspace(T, 64, 64, E, k)
+    counts, offsets, perm, inv, xpq, sxp = moe.moe_permute_int8(idx.to(DEV), xq, sx, E, ws)
+    for pos in (0, T * k // 2 + 17, T * k - 1):
+        t = int(perm[pos]) // k
+        assert torch.equal(xpq[pos], xq[t]) and float(sxp[pos]) == float(sx[t])
+    del xpq
+    y = torch.empty(T * k, d, dtype=torch.bfloat16, device=DEV)
+    y.copy_(torch.arange(T * k, device=DEV)[:, None].remainder(251))
+    w = wl.random_gates(T, k, 23).to(DEV)
+    dout = R.randn(24, T, d).to(DEV)
+    out = moe.moe_combine_weighted(y, inv, w)
+    dx = moe.moe_permute_backward(y, inv, T, k)
+    for t in (0, T // 2 + 3, T - 1):
+        rows = inv.view(T, k)[t].long()
+        ref = (y[rows].double() * w[t].double()[:, None]).sum(0)
+        R.within(out[t], ref, R.BF16 * ref + 18 * R.F32 * ref, "combine")
+        ref = y[rows].double().sum(0)
+        R.within(dx[t], ref, R.BF16 * ref + 18 * R.F32 * ref, "permute backward")
+    dy, dw = moe.moe_combine_weighted_backward(dout, y, inv, w, dy_p=y)
+    for t in (0, T - 1):
+        rows = inv.view(T, k)[t].long()
+        ref = w[t].double()[:, None] * dout[t].double()
+        R.within(dy[rows], ref, (R.BF16 + R.F32) * ref.abs() + R.TINY, "dy_p")
+
+
 def test_permute_int8_agrees_with_moe_permute():
     T, E, k, d = 515, 64, 8, 256
     idx = _routing(T, E, k, 9).to(DEV)

@@ -2,6 +2,8 @@
 gradient formulas against differences and against automatic differentiation, and their workspace size."""
 
 import ctypes as C
+import os
+import subprocess
 
 import pytest
 import torch
@@ -224,3 +226,70 @@ def test_int8_scale_rule():
     v, scale = R.int8_rows(y)
     assert scale.tolist() == [1.0, 1.0, 1.0 / 127]
     assert torch.round(v).tolist() == [[127, -127, 64, 0], [0, 0, 0, 0], [127, -64, 32, 0]]
+
+
+# ---------------------------------------------------------------- how a dense int8 product is cut
+
+@pytest.fixture(scope="module")
+def shape_of(tmp_path_factory):
+    here = os.path.dirname(os.path.abspath(__file__))
+    out = str(tmp_path_factory.mktemp("shape") / "libshape.so")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-o", out,
+                    os.path.join(here, "int8_shape_harness.cpp")], check=True)
+    lib = C.CDLL(out)
+    i64 = C.c_int64
+    lib.int8_shape_of.argtypes = [i64, i64, i64, C.c_int, C.c_int, C.c_int, C.POINTER(i64)]
+    lib.int8_grouped_pair_of.argtypes = [i64, i64, i64, i64, C.c_int, C.c_int, C.c_int]
+
+    def f(T, K, N, sms=148, can_pair=True, pairs=-1):
+        buf = (i64 * 5)()
+        lib.int8_shape_of(T, K, N, sms, int(can_pair), pairs, buf)
+        return tuple(buf)
+    f.grouped = lib.int8_grouped_pair_of
+    return f
+
+
+SINGLE, PAIR, SPLIT = 0, 1, 2
+
+
+@pytest.mark.parametrize("sms,can_pair,pairs", [(148, True, -1), (148, True, 0), (148, True, 1), (148, False, 1),
+                                                (148, False, -1), (1, True, -1), (7, False, -1)])
+def test_int8_cut_covers_the_product(shape_of, sms, can_pair, pairs):
+    """Every cut: the units cover the rows, tiles fit the accumulator and the form's alignment, and CTAs that share a
+    tile have a K block each and are all resident at once."""
+    for T in (1, 2, 15, 16, 17, 33, 100, 255, 256, 257, 1000, 4096, 16385, 1 << 20):
+        for K in (64, 128, 192, 1024, 7168, 65536):
+            for N in (64, 128, 192, 2048, 7168, 65536):
+                form, chunk, units, split, tiles = shape_of(T, K, N, sms, can_pair, pairs)
+                what = (T, K, N, form, chunk, units, split, tiles)
+                assert form in (SINGLE, PAIR, SPLIT), what
+                assert chunk % (32 if form == PAIR else 16) == 0 and 16 <= chunk <= 256, what
+                assert (units - 1) * chunk < T <= units * chunk, what
+                rows = 256 if form == PAIR else 128
+                assert tiles == -(-N // rows) * units, what
+                if form == SPLIT:
+                    assert split in (2, 4, 8) and split <= -(-K // 128) and tiles * split <= sms, what
+                else:
+                    assert split == 1, what
+                if pairs == 1 and can_pair:
+                    assert form == PAIR, what
+                if pairs == 0 or not can_pair:
+                    assert form != PAIR, what
+
+
+def test_int8_cut_reaches_every_form(shape_of):
+    forms = {shape_of(T, K, N)[0] for T, K, N in ((8, 1024, 2048), (8, 7168, 4096), (8192, 7168, 4096))}
+    assert forms == {SINGLE, PAIR, SPLIT}
+    assert {shape_of(1, K, N)[3] for K, N in ((7168, 7168), (7168, 4096), (16384, 512))} == {2, 4, 8}
+    # rows of a tile shrink until the SMs are busy
+    assert shape_of(256, 1024, 2048)[1] < 256 and shape_of(8192, 1024, 2048)[1] >= 192
+    # more tiles than a launch counts are refused (units 0), not wrapped
+    assert shape_of((1 << 31) - 1, 64, (1 << 31) - 64)[2] == 0
+
+
+def test_grouped_int8_takes_pairs_for_wide_segments(shape_of):
+    g = shape_of.grouped
+    assert g(4096 * 8, 2048, 2048, 64, 148, 1, -1) == 1
+    assert g(32 * 8, 2048, 2048, 64, 148, 1, -1) == 0
+    assert g(4096 * 8, 2048, 2048, 64, 148, 0, -1) == 0 and g(4096 * 8, 2048, 2048, 64, 148, 0, 1) == 0
+    assert g(1, 64, 64, 1, 148, 1, 1) == 1 and g(1 << 20, 2048, 2048, 8, 148, 1, 0) == 0
