@@ -436,13 +436,16 @@ def _need(ok: bool, what: str) -> None:
         raise AssertionError(what)
 
 
-def _tensors(dtype, *named):
-    """Each (tensor, shape, name): contiguous, on the current device, of this dtype and shape."""
+def _tensors(*named):
+    """Each (tensor, dtype, shape, name): contiguous, on the current device, of this dtype and shape."""
     dev = torch.cuda.current_device()
-    for t, shape, name in named:
+    for t, dtype, shape, name in named:
         if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
             raise AssertionError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, "
                                  f"got {t.dtype} {tuple(t.shape)}, strides {tuple(t.stride())}, on {t.device}")
+
+
+_BF16, _F32, _I32, _I8, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.uint8
 
 
 def _rows_of(t: torch.Tensor, name: str):
@@ -486,16 +489,16 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _norm_args(x, weight, residual, xsum, y):
     T, d = rows = _rows_of(x, "x")
-    named = [(x, rows, "x"), (weight, (d,), "weight")]
+    named = [(x, _BF16, rows, "x"), (weight, _BF16, (d,), "weight")]
     if residual is not None:
-        named.append((residual, rows, "residual"))
+        named.append((residual, _BF16, rows, "residual"))
     else:
         _need(xsum is None, "xsum is the sum with a residual; there is none")
     if xsum is not None:
-        named.append((xsum, rows, "xsum"))
+        named.append((xsum, _BF16, rows, "xsum"))
     if y is not None:
-        named.append((y, rows, "y"))
-    _tensors(torch.bfloat16, *named)
+        named.append((y, _BF16, rows, "y"))
+    _tensors(*named)
     return T, d
 
 
@@ -548,16 +551,16 @@ def moe_rmsnorm_backward(dy, xsum, weight, eps: float, dxsum=None, dx=None, dwei
     ``dxsum``: the gradient that reaches the stream itself.  ``ws``: a uint8 tensor of
     moe_rmsnorm_backward_workspace_size bytes, made here when not given."""
     T, d = rows = _rows_of(dy, "dy")
-    named = [(dy, rows, "dy"), (xsum, rows, "xsum"), (weight, (d,), "weight")]
+    named = [(dy, _BF16, rows, "dy"), (xsum, _BF16, rows, "xsum"), (weight, _BF16, (d,), "weight")]
     if dxsum is not None:
-        named.append((dxsum, rows, "dxsum"))
+        named.append((dxsum, _BF16, rows, "dxsum"))
     if dx is not None:
-        named.append((dx, rows, "dx"))
-    _tensors(torch.bfloat16, *named)
+        named.append((dx, _BF16, rows, "dx"))
     if dweight is not None:
-        _tensors(torch.float32, (dweight, (d,), "dweight"))
+        named.append((dweight, _F32, (d,), "dweight"))
     if ws is not None:
-        _tensors(torch.uint8, (ws, (ws.numel(),), "ws"))
+        named.append((ws, _U8, (ws.numel(),), "ws"))
+    _tensors(*named)
     with _on(stream):
         if dx is None:
             dx = torch.empty_like(dy)
@@ -573,7 +576,7 @@ def moe_rmsnorm_backward(dy, xsum, weight, eps: float, dxsum=None, dx=None, dwei
 def moe_quantize_int8_rows(x: torch.Tensor, stream=None):
     """One scale a row: bf16 [R, C] (or [E, R, C], taken as [E*R, C]) -> (int8 codes, fp32 scales, one a row)."""
     _need(x.dim() >= 2, "x: expected 2 dimensions or more")
-    _tensors(torch.bfloat16, (x, x.shape, "x"))
+    _tensors((x, _BF16, x.shape, "x"))
     Cc = x.shape[-1]
     R = x.numel() // Cc if Cc else 0
     with _on(stream):
@@ -585,15 +588,15 @@ def moe_quantize_int8_rows(x: torch.Tensor, stream=None):
 def moe_gemm_int8(xq, sx, Wq, sw, ws: torch.Tensor, out=None, stream=None):
     """out [T,N] bf16 = (xq [T,K] Wq [N,K]^T) * sx [T] * sw [N]; ``ws``: any initialised workspace."""
     (T, K), (N, _) = _rows_of(xq, "xq"), _rows_of(Wq, "Wq")
-    _tensors(torch.int8, (xq, (T, K), "xq"), (Wq, (N, K), "Wq"))
-    _tensors(torch.float32, (sx, (T,), "sx"), (sw, (N,), "sw"))
-    _tensors(torch.uint8, (ws, (ws.numel(),), "ws"))
+    n = ws.numel()
+    _tensors((xq, _I8, (T, K), "xq"), (Wq, _I8, (N, K), "Wq"), (sx, _F32, (T,), "sx"), (sw, _F32, (N,), "sw"),
+             (ws, _U8, (n,), "ws"))
     if out is None:
         with _on(stream):
             out = xq.new_empty((T, N), dtype=torch.bfloat16)
     else:
-        _tensors(torch.bfloat16, (out, (T, N), "out"))
-    _call("moe_gemm_int8", _ptr(xq), _ptr(sx), _ptr(Wq), _ptr(sw), T, K, N, _ptr(out), _ptr(ws), ws.numel(),
+        _tensors((out, _BF16, (T, N), "out"))
+    _call("moe_gemm_int8", _ptr(xq), _ptr(sx), _ptr(Wq), _ptr(sw), T, K, N, _ptr(out), _ptr(ws), n,
           _queue(stream))
     return out
 
@@ -605,17 +608,16 @@ def moe_grouped_gemm_int8(xpq, sxp, counts, offsets, Wq, sw, T: int, k: int, ws:
     _need(Wq.dim() == 3, "Wq: expected [E, N, K]")
     E, N, _ = Wq.shape
     _need(P == T * k, f"xpq: expected {T} * {k} rows, got {P}")
-    _tensors(torch.int8, (xpq, (P, K), "xpq"), (Wq, (E, N, K), "Wq"))
-    _tensors(torch.float32, (sxp, (P,), "sxp"), (sw, (E, N), "sw"))
-    _tensors(torch.int32, (counts, (E,), "counts"), (offsets, (E + 1,), "offsets"))
-    _tensors(torch.uint8, (ws, (ws.numel(),), "ws"))
+    n = ws.numel()
+    _tensors((xpq, _I8, (P, K), "xpq"), (Wq, _I8, (E, N, K), "Wq"), (sxp, _F32, (P,), "sxp"), (sw, _F32, (E, N), "sw"),
+             (counts, _I32, (E,), "counts"), (offsets, _I32, (E + 1,), "offsets"), (ws, _U8, (n,), "ws"))
     if out is None:
         with _on(stream):
             out = xpq.new_empty((P, N), dtype=torch.bfloat16)
     else:
-        _tensors(torch.bfloat16, (out, (P, N), "out"))
+        _tensors((out, _BF16, (P, N), "out"))
     _call("moe_grouped_gemm_int8", _ptr(xpq), _ptr(sxp), _ptr(counts), _ptr(offsets), _ptr(Wq), _ptr(sw), T, K, N, E, k,
-          _ptr(out), _ptr(ws), ws.numel(), _queue(stream))
+          _ptr(out), _ptr(ws), n, _queue(stream))
     return out
 
 
@@ -624,10 +626,8 @@ def moe_permute_int8(topk_idx, xq, sx, E: int, ws: torch.Tensor, stream=None):
     Rows of xpq and sxp past offsets[E] are unset."""
     (T, k), (_, d) = _rows_of(topk_idx, "topk_idx"), _rows_of(xq, "xq")
     P = T * k
-    _tensors(torch.int32, (topk_idx, (T, k), "topk_idx"))
-    _tensors(torch.int8, (xq, (T, d), "xq"))
-    _tensors(torch.float32, (sx, (T,), "sx"))
-    _tensors(torch.uint8, (ws, (ws.numel(),), "ws"))
+    _tensors((topk_idx, _I32, (T, k), "topk_idx"), (xq, _I8, (T, d), "xq"), (sx, _F32, (T,), "sx"),
+             (ws, _U8, (ws.numel(),), "ws"))
     with _on(stream):
         counts, offsets, perm, inv = (topk_idx.new_empty(n) for n in (E, E + 1, P, P))
         xpq, sxp = xq.new_empty((P, d)), sx.new_empty(P)
@@ -641,14 +641,12 @@ def moe_permute_int8(topk_idx, xq, sx, E: int, ws: torch.Tensor, stream=None):
 def moe_combine_weighted(y_p, inv_perm, topk_w, shared_out=None, out=None, stream=None):
     """out[t] = sum_j topk_w[t,j] y_p[inv_perm[t*k+j]] (+ shared_out[t]); T and k are topk_w's."""
     (T, k), (P, d) = _rows_of(topk_w, "topk_w"), _rows_of(y_p, "y_p")
-    named = [(y_p, (T * k, d), "y_p")]
+    named = [(y_p, _BF16, (T * k, d), "y_p"), (topk_w, _F32, (T, k), "topk_w"), (inv_perm, _I32, (T * k,), "inv_perm")]
     if shared_out is not None:
-        named.append((shared_out, (T, d), "shared_out"))
+        named.append((shared_out, _BF16, (T, d), "shared_out"))
     if out is not None:
-        named.append((out, (T, d), "out"))
-    _tensors(torch.bfloat16, *named)
-    _tensors(torch.float32, (topk_w, (T, k), "topk_w"))
-    _tensors(torch.int32, (inv_perm, (T * k,), "inv_perm"))
+        named.append((out, _BF16, (T, d), "out"))
+    _tensors(*named)
     if out is None:
         with _on(stream):
             out = y_p.new_empty((T, d))
@@ -661,14 +659,13 @@ def moe_combine_weighted_backward(dout, y_p, inv_perm, topk_w, dy_p=None, dw=Non
     """(dy_p [T*k,d] bf16, dw [T,k] fp32) of moe_combine_weighted; ``dy_p`` may be ``y_p``.
     Rows of a new dy_p that no pair has (dropped pairs) are zero only if the caller gives them so."""
     (T, k), (P, d) = _rows_of(topk_w, "topk_w"), _rows_of(y_p, "y_p")
-    named = [(dout, (T, d), "dout"), (y_p, (T * k, d), "y_p")]
+    named = [(dout, _BF16, (T, d), "dout"), (y_p, _BF16, (T * k, d), "y_p"), (topk_w, _F32, (T, k), "topk_w"),
+             (inv_perm, _I32, (T * k,), "inv_perm")]
     if dy_p is not None:
-        named.append((dy_p, (T * k, d), "dy_p"))
-    _tensors(torch.bfloat16, *named)
-    _tensors(torch.float32, (topk_w, (T, k), "topk_w"))
-    _tensors(torch.int32, (inv_perm, (T * k,), "inv_perm"))
+        named.append((dy_p, _BF16, (T * k, d), "dy_p"))
     if dw is not None:
-        _tensors(torch.float32, (dw, (T, k), "dw"))
+        named.append((dw, _F32, (T, k), "dw"))
+    _tensors(*named)
     with _on(stream):
         if dy_p is None:
             dy_p = torch.empty_like(y_p)
@@ -682,13 +679,12 @@ def moe_combine_weighted_backward(dout, y_p, inv_perm, topk_w, dy_p=None, dw=Non
 def moe_permute_backward(dxp, inv_perm, T: int, k: int, addend=None, dx=None, stream=None):
     """dx [T,d] bf16 of moe_permute: dx[t] = sum_j dxp[inv_perm[t*k+j]] (+ addend[t])."""
     P, d = _rows_of(dxp, "dxp")
-    named = [(dxp, (T * k, d), "dxp")]
+    named = [(dxp, _BF16, (T * k, d), "dxp"), (inv_perm, _I32, (T * k,), "inv_perm")]
     if addend is not None:
-        named.append((addend, (T, d), "addend"))
+        named.append((addend, _BF16, (T, d), "addend"))
     if dx is not None:
-        named.append((dx, (T, d), "dx"))
-    _tensors(torch.bfloat16, *named)
-    _tensors(torch.int32, (inv_perm, (T * k,), "inv_perm"))
+        named.append((dx, _BF16, (T, d), "dx"))
+    _tensors(*named)
     if dx is None:
         with _on(stream):
             dx = dxp.new_empty((T, d))
