@@ -24,8 +24,13 @@
 //
 // Warp roles: warp 0 TMA producer, warp 1 MMA issuer, warps 2-9 epilogue (two a
 // TMEM lane quadrant, every other 16 columns each); two TMEM accumulators of 256
-// columns; every wait is bounded.  All loads come after griddepcontrol.wait: weights may be the output
-// of the kernel before (a quantiser).
+// columns; every wait is bounded.  All loads come after griddepcontrol.wait: the
+// weights may be the output of the kernel before (a quantiser).
+//
+// Bound: at prefill the tensor cores, under the power cap (T=4096 K=7168 N=4096 on
+// one B200: 77 us, 3.1 PTOP/s, tensor pipe 71% active); at K = 2048 and below the
+// epilogue's stores beside the loads (T=8192 N=7168 98 us, 2.5 PTOP/s; without its
+// stores 74); at decode HBM (64 experts K=N=2048, 256 rows: 42 us, 6.5 TB/s).
 #pragma once
 
 #include "common.cuh"

@@ -52,6 +52,24 @@ def test_permute_int8(T, E, k, d, drop):
     assert torch.equal(g[4][:n], xq[tok]) and torch.equal(g[5][:n], sx[tok])
 
 
+@pytest.mark.parametrize("T", [3, 128, 500])
+def test_permute_int8_of_one_expert_chosen_more_than_once(T):
+    """The same expert in several of a token's places: every pair keeps a position of its own, in order."""
+    E, k, d = 8, 4, 128
+    idx = torch.full((T, k), 5, dtype=torch.int32)
+    idx[:, 1] = 2
+    counts, offsets, perm, inv = R.permutation(idx, E)
+    xq, sx = R.codes(25, T, d), R.scales(26, T)
+    ws = moe.new_workspace(T, 64, 64, E, k)
+    g = [t.cpu() for t in moe.moe_permute_int8(idx.to(DEV), xq.to(DEV), sx.to(DEV), E, ws)]
+    assert torch.equal(g[0], counts) and torch.equal(g[1], offsets) and torch.equal(g[2], perm) and torch.equal(g[3], inv)
+    assert torch.equal(g[4], xq[perm.long() // k]) and torch.equal(g[5], sx[perm.long() // k])
+    wq, sw = R.codes(27, E, 128, d).to(DEV), R.scales(28, E, 128, mean=0.001).to(DEV)
+    out = moe.moe_grouped_gemm_int8(*(t.to(DEV) for t in (g[4], g[5], g[0], g[1])), wq, sw, T, k, ws)
+    ref = R.int8_gemm(g[4][T:].to(DEV), g[5][T:].to(DEV), wq[5], sw[5])
+    R.within(out[T:], ref, (R.BF16 + 2.0 ** -21) * ref.abs() + R.TINY, "the chosen expert")
+
+
 @pytest.mark.parametrize("T", [32768, 32769, 45000])
 def test_permute_int8_of_many_pairs(T):
     """Around 2^18 pairs, where another way of finding the positions takes over."""
