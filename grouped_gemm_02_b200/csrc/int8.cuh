@@ -17,7 +17,7 @@
 //   I8_PAIR    CTA pairs (cta_group::2): 256 channels a tile, each CTA loads its
 //              128 channels and half of the rows -- two thirds of the shared
 //              memory traffic per MMA, which bounds wide tiles of 8-bit operands
-//   I8_SPLIT   a cluster of 2, 4 or 8 CTAs shares one tile's K range and adds
+//   I8_SPLIT   a cluster of 2 to 8 CTAs shares one tile's K range and adds
 //              the int32 sums through distributed shared memory: dense products
 //              with fewer tiles than SMs, bound by the weights' bytes.  The sums
 //              are integers, so the split changes no bit.
@@ -165,8 +165,8 @@ __device__ __forceinline__ bool i8_plan(const Int8Args& a, I8Plan* p, int mt, in
             const int units = __reduce_add_sync(0xffffffffu, u[i]);
             const int w = min(256 >> i, max(most, 1));
             const float waves = (float)(((int64_t)units * mt + slots - 1) / slots);
-            const float kb = fmaxf((128.f + (pair ? 0.5f : 1.f) * (float)w) * (128.f / 90.f), 1.5f * (float)w);
-            const float cost = waves * ((float)nk * kb + 170.f + 15.f * (float)w);
+            const float kb = fmaxf((128.f + (pair ? 0.5f : 1.f) * (float)w) * (128.f / 92.f), 1.4f * (float)w);
+            const float cost = waves * ((float)nk * kb + 215.f) + 7.f * (float)w;
             if (i == 0 || cost < least) {
                 least = cost;
                 cap = 256 >> i;

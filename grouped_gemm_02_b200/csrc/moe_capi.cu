@@ -43,7 +43,7 @@ struct DeviceState {
     int sm_count = 0;
     int pair_grid = 0;       // CTAs of a CTA-pair GEMM launch: 2 x the clusters that fit at once (0: none)
     int fp8_pair_grid = 0;   // the same for the FP8 / FP4 GEMM
-    int i8_pair_grid = 0;    // the same for the int8 product
+    Int8Device i8;           // what the int8 products can use: SMs, and the clusters that fit at once
 };
 
 std::mutex g_mu;
@@ -110,17 +110,17 @@ cudaError_t launch_pair(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t 
     return launch_cluster(kernel, 2, grid, block, smem, st, std::forward<Args>(args)...);
 }
 
-// How many clusters of two CTAs of `kernel` can be resident at once (0 on error).
+// How many clusters of `ctas` CTAs of `kernel` can be resident at once (0 on error).
 template <typename... KArgs>
-int max_pair_clusters(void (*kernel)(KArgs...), size_t smem, int threads = kGemmThreads)
+int max_clusters(void (*kernel)(KArgs...), size_t smem, int threads = kGemmThreads, int ctas = 2)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
+    cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = ctas;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -198,19 +198,22 @@ int device_setup(DeviceState** out)
                 return MOE_ERR_CUDA;
             // CTA pairs: a grid of exactly the clusters that fit at once, so the
             // persistent pairs all start together (the same count for every mode)
-            int pc = max_pair_clusters(grouped_gemm_kernel<MODE_GATED, true>, kGemmSmemBytes);
-            pc = std::min(pc, max_pair_clusters(grouped_gemm_kernel<MODE_DOWN, true>, kGemmSmemBytes));
-            pc = std::min(pc, max_pair_clusters(grouped_gemm_kernel<MODE_FUSED, true>, kGemmSmemBytes));
+            int pc = max_clusters(grouped_gemm_kernel<MODE_GATED, true>, kGemmSmemBytes);
+            pc = std::min(pc, max_clusters(grouped_gemm_kernel<MODE_DOWN, true>, kGemmSmemBytes));
+            pc = std::min(pc, max_clusters(grouped_gemm_kernel<MODE_FUSED, true>, kGemmSmemBytes));
             st.pair_grid = 2 * std::min(pc, sms / 2);
-            int pc8 = max_pair_clusters(grouped_gemm_fp8_kernel<FP8_GATED, false, true>, kFp8SmemBytes, kFp8Threads);
-            pc8 = std::min(pc8, max_pair_clusters(grouped_gemm_fp8_kernel<FP8_DOWN, false, true>, kFp8SmemBytes,
+            int pc8 = max_clusters(grouped_gemm_fp8_kernel<FP8_GATED, false, true>, kFp8SmemBytes, kFp8Threads);
+            pc8 = std::min(pc8, max_clusters(grouped_gemm_fp8_kernel<FP8_DOWN, false, true>, kFp8SmemBytes,
                                                   kFp8Threads));
-            pc8 = std::min(pc8, max_pair_clusters(grouped_gemm_fp8_kernel<FP8_GATED, true, true>, kFp8SmemBytes,
+            pc8 = std::min(pc8, max_clusters(grouped_gemm_fp8_kernel<FP8_GATED, true, true>, kFp8SmemBytes,
                                                   kFp8Threads));
-            pc8 = std::min(pc8, max_pair_clusters(grouped_gemm_fp8_kernel<FP8_DOWN, true, true>, kFp8SmemBytes,
+            pc8 = std::min(pc8, max_clusters(grouped_gemm_fp8_kernel<FP8_DOWN, true, true>, kFp8SmemBytes,
                                                   kFp8Threads));
             st.fp8_pair_grid = 2 * std::min(pc8, sms / 2);
-            st.i8_pair_grid = 2 * std::min(max_pair_clusters(int8_gemm_kernel<I8_PAIR>, kI8SmemBytes, kI8Threads), sms / 2);
+            st.i8.sms = sms;
+            st.i8.pairs = std::min(max_clusters(int8_gemm_kernel<I8_PAIR>, kI8SmemBytes, kI8Threads), sms / 2);
+            for (int i = 2; i <= kI8MaxSplit; i++)
+                st.i8.clusters[i] = max_clusters(int8_gemm_kernel<I8_SPLIT>, kI8SmemBytes, kI8Threads, i);
             if (!g_encode) {
                 cudaDriverEntryPointQueryResult q;
                 void* fn = nullptr;
@@ -1450,7 +1453,7 @@ int run_int8(const Int8Args& a, const void* xq, int64_t rows, const void* Wq, in
     const dim3 block(kI8Threads);
     if (form == I8_PAIR)
         return status_of(launch_cluster(int8_gemm_kernel<I8_PAIR>, 2,
-                                        dim3((unsigned)std::min<int64_t>(2 * tiles, dev->i8_pair_grid)), block,
+                                        dim3((unsigned)(2 * std::min<int64_t>(tiles, dev->i8.pairs))), block,
                                         kI8SmemBytes, st, ma, mb16, mb64, a));
     if (form == I8_SPLIT)
         return status_of(launch_cluster(int8_gemm_kernel<I8_SPLIT>, split, dim3((unsigned)tiles * split), block,
@@ -1576,8 +1579,7 @@ int moe_gemm_int8(const int8_t* xq, const float* sx, const int8_t* Wq, const flo
     a.sw = sw;
     a.out = reinterpret_cast<bf16*>(out);
     a.err = static_cast<uint32_t*>(ws);
-    const Int8Shape sh = i8_shape(T, K, N, dev->sm_count, dev->i8_pair_grid >= 2,
-                                  policy(g_policy_pair, "MOE_GEMM_PAIR", /*invert=*/false));
+    const Int8Shape sh = i8_shape(T, K, N, dev->i8, policy(g_policy_pair, "MOE_GEMM_PAIR", /*invert=*/false));
     if (sh.units == 0) return MOE_ERR_ARG;   // more tiles than a launch can count
     a.chunk = sh.chunk;
     a.units = sh.units;
@@ -1599,8 +1601,8 @@ int moe_grouped_gemm_int8(const int8_t* xpq, const float* sxp, const int32_t* co
     DeviceState* dev;
     if ((rc = device_setup(&dev))) return rc;
     const int64_t P = T * k;
-    const bool pair = i8_grouped_pair(P, K, N, E, dev->sm_count, dev->i8_pair_grid >= 2,
-                                      policy(g_policy_pair, "MOE_GEMM_PAIR", /*invert=*/false));
+    const bool pair =
+        i8_grouped_pair(P, K, N, E, dev->i8, policy(g_policy_pair, "MOE_GEMM_PAIR", /*invert=*/false));
     Int8Args a{};
     a.counts = counts;
     a.offsets = offsets;

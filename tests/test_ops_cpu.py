@@ -238,29 +238,31 @@ def shape_of(tmp_path_factory):
                     os.path.join(here, "int8_shape_harness.cpp")], check=True)
     lib = C.CDLL(out)
     i64 = C.c_int64
-    lib.int8_shape_of.argtypes = [i64, i64, i64, C.c_int, C.c_int, C.c_int, C.POINTER(i64)]
+    lib.int8_shape_of.argtypes = [i64, i64, i64, C.c_int, C.c_int, C.POINTER(C.c_int), C.c_int, C.POINTER(i64)]
     lib.int8_grouped_pair_of.argtypes = [i64, i64, i64, i64, C.c_int, C.c_int, C.c_int]
 
-    def f(T, K, N, sms=148, can_pair=True, pairs=-1):
+    def f(T, K, N, sms=148, can_pair=True, pairs=-1, clusters=B200_CLUSTERS):
         buf = (i64 * 5)()
-        lib.int8_shape_of(T, K, N, sms, int(can_pair), pairs, buf)
+        lib.int8_shape_of(T, K, N, sms, int(can_pair), (C.c_int * 9)(*clusters), pairs, buf)
         return tuple(buf)
     f.grouped = lib.int8_grouped_pair_of
     return f
 
 
 SINGLE, PAIR, SPLIT = 0, 1, 2
+B200_CLUSTERS = (0, 148, 74, 45, 33, 26, 22, 15, 15)       # of 0..8 CTAs that fit a B200 at once
 
 
-@pytest.mark.parametrize("sms,can_pair,pairs", [(148, True, -1), (148, True, 0), (148, True, 1), (148, False, 1),
-                                                (148, False, -1), (1, True, -1), (7, False, -1)])
-def test_int8_cut_covers_the_product(shape_of, sms, can_pair, pairs):
+@pytest.mark.parametrize("sms,can_pair,pairs,clusters", [
+    (148, True, -1, B200_CLUSTERS), (148, True, 0, B200_CLUSTERS), (148, True, 1, B200_CLUSTERS),
+    (148, False, 1, B200_CLUSTERS), (148, False, -1, (0,) * 9), (1, True, -1, (0,) * 9), (7, False, -1, (0, 7, 3, 2, 1, 1, 1, 1, 0))])
+def test_int8_cut_covers_the_product(shape_of, sms, can_pair, pairs, clusters):
     """Every cut: the units cover the rows, tiles fit the accumulator and the form's alignment, and CTAs that share a
     tile have a K block each and are all resident at once."""
     for T in (1, 2, 15, 16, 17, 33, 100, 255, 256, 257, 1000, 4096, 16385, 1 << 20):
         for K in (64, 128, 192, 1024, 7168, 65536):
             for N in (64, 128, 192, 2048, 7168, 65536):
-                form, chunk, units, split, tiles = shape_of(T, K, N, sms, can_pair, pairs)
+                form, chunk, units, split, tiles = shape_of(T, K, N, sms, can_pair, pairs, clusters)
                 what = (T, K, N, form, chunk, units, split, tiles)
                 assert form in (SINGLE, PAIR, SPLIT), what
                 assert chunk % (32 if form == PAIR else 16) == 0 and 16 <= chunk <= 256, what
@@ -268,7 +270,7 @@ def test_int8_cut_covers_the_product(shape_of, sms, can_pair, pairs):
                 rows = 256 if form == PAIR else 128
                 assert tiles == -(-N // rows) * units, what
                 if form == SPLIT:
-                    assert split in (2, 4, 8) and split <= -(-K // 128) and tiles * split <= sms, what
+                    assert 2 <= split <= 8 and split <= -(-K // 128) and tiles <= clusters[split], what
                 else:
                     assert split == 1, what
                 if pairs == 1 and can_pair:
@@ -280,7 +282,7 @@ def test_int8_cut_covers_the_product(shape_of, sms, can_pair, pairs):
 def test_int8_cut_reaches_every_form(shape_of):
     forms = {shape_of(T, K, N)[0] for T, K, N in ((8, 1024, 2048), (8, 7168, 4096), (8192, 7168, 4096))}
     assert forms == {SINGLE, PAIR, SPLIT}
-    assert {shape_of(1, K, N)[3] for K, N in ((7168, 7168), (7168, 4096), (16384, 512))} == {2, 4, 8}
+    assert [shape_of(1, K, N)[3] for K, N in ((7168, 7168), (7168, 4096), (16384, 512))] == [2, 4, 8]
     # rows of a tile shrink until the SMs are busy
     assert shape_of(256, 1024, 2048)[1] < 256 and shape_of(8192, 1024, 2048)[1] >= 192
     # more tiles than a launch counts are refused (units 0), not wrapped
