@@ -5,8 +5,9 @@
 //
 // of one weight matrix for every row (dense, e = 0) or of expert e's matrix for
 // the rows offsets[e] .. offsets[e + 1) (grouped).  The sum is exact: a product
-// is at most 2^14, so K <= 2^16 keeps it below 2^30; it is rounded to fp32 once,
-// scaled in fp32 and rounded to bf16 once.
+// is at most 2^14, so K <= 2^16 keeps it at 2^30 at most; it is rounded to fp32
+// once, scaled in fp32 (by the channel first: a row's scale may be near the end of
+// the range, a weight's is not) and rounded to bf16 once.
 //
 // As in the bf16 expert GEMM the weights fill the M slot (128 channels) and the
 // rows the N slot (16..256), so a decode batch costs a 16-wide MMA.  A K block is
@@ -475,10 +476,10 @@ __global__ void __launch_bounds__(kI8Threads, 1)
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
                         const float4 sc = reinterpret_cast<const float4*>(s_sx + c0)[j];
-                        const __nv_bfloat162 lo = __floats2bfloat162_rn((float)(int)v[4 * j] * sc.x * sw,
-                                                                        (float)(int)v[4 * j + 1] * sc.y * sw);
-                        const __nv_bfloat162 hi = __floats2bfloat162_rn((float)(int)v[4 * j + 2] * sc.z * sw,
-                                                                        (float)(int)v[4 * j + 3] * sc.w * sw);
+                        const __nv_bfloat162 lo = __floats2bfloat162_rn((float)(int)v[4 * j] * sw * sc.x,
+                                                                        (float)(int)v[4 * j + 1] * sw * sc.y);
+                        const __nv_bfloat162 hi = __floats2bfloat162_rn((float)(int)v[4 * j + 2] * sw * sc.z,
+                                                                        (float)(int)v[4 * j + 3] * sw * sc.w);
                         w[2 * j] = *reinterpret_cast<const uint32_t*>(&lo);
                         w[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&hi);
                     }
@@ -537,8 +538,8 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 }
                 const float sx = __ldg(a.sx + tl.row0 + col);
                 const float4 sw = __ldg(reinterpret_cast<const float4*>(a.sw + ch));
-                __nv_bfloat162 lo = __floats2bfloat162_rn((float)sum[0] * sx * sw.x, (float)sum[1] * sx * sw.y);
-                __nv_bfloat162 hi = __floats2bfloat162_rn((float)sum[2] * sx * sw.z, (float)sum[3] * sx * sw.w);
+                __nv_bfloat162 lo = __floats2bfloat162_rn((float)sum[0] * sw.x * sx, (float)sum[1] * sw.y * sx);
+                __nv_bfloat162 hi = __floats2bfloat162_rn((float)sum[2] * sw.z * sx, (float)sum[3] * sw.w * sx);
                 *reinterpret_cast<uint2*>(a.out + (size_t)(tl.row0 + col) * a.N + ch) =
                     make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
             }

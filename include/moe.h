@@ -314,7 +314,7 @@ MOE_API int moe_quantize_int8_rows(const moe_bf16 *x, int64_t rows, int64_t cols
 
 /* out [T,N] = bf16( (xq Wq^T)[t,n] * sx[t] * sw[n] ): xq [T,K], sx [T], Wq [N,K],
  * sw [N].  The integer sum is exact (codes -128..127); it is converted to fp32
- * and scaled there.  K and N multiples of 64, K at most 65536.  `ws` (at least
+ * and scaled there, by sw and then by sx.  K and N multiples of 64, K at most 65536.  `ws` (at least
  * 256 bytes, initialised like every workspace) supplies the device error word
  * and holds nothing else of this call. */
 MOE_API int moe_gemm_int8(const int8_t *xq, const float *sx, const int8_t *Wq, const float *sw, int64_t T, int64_t K,

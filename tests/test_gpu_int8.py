@@ -122,6 +122,18 @@ def test_gemm_int8_special_scales():
     R.within(out[4, keep], ref[4, keep], REL * ref[4, keep].abs(), "a plain row")
 
 
+@pytest.mark.parametrize("T,K,N", [(5, 256, 128), (3, 7168, 2048), (700, 2048, 4096)])
+def test_gemm_int8_scales_near_the_ends_of_the_range(T, K, N):
+    """Rows quantised from values around 1e38 and 1e-30: the result is in range wherever its value is."""
+    xq, sx, wq, sw = _dense(T, K, N, seed=78)
+    sx[0], sx[1], sx[T - 1] = 2.6e36, 1e-32, 1e33
+    sw *= 1e-4
+    out = moe.moe_gemm_int8(xq.to(DEV), sx.to(DEV), wq.to(DEV), sw.to(DEV), _ws(T))
+    ref = R.int8_gemm(xq.to(DEV), sx.to(DEV), wq.to(DEV), sw.to(DEV))
+    assert ref.abs().max() < 3e38
+    R.within(out, ref, REL * ref.abs() + R.TINY, "far scales")
+
+
 def test_gemm_int8_empty_and_refusals():
     wq, sw = R.codes(1, 128, 256).to(DEV), R.scales(2, 128).to(DEV)
     ws = _ws(4)
