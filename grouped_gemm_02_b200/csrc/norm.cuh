@@ -15,8 +15,10 @@
 // Bound: HBM.  Every input is read once and every output written once: a row
 // stays in the registers of one group of warps between the reduction and the
 // normalisation.  T=16384 d=7168 with a residual on one B200: bf16 138 us (6.8
-// TB/s), e4m3 133 us (6.2 TB/s), int8 140 us (5.9 TB/s); the gradient at T=4099
-// d=7168 45 us (5.3 TB/s).
+// TB/s), e4m3 133 us (6.2 TB/s), int8 136 us (6.0 TB/s); the gradient at T=4099
+// d=7168 42 us (5.6 TB/s).  Next to the bytes it is the instructions that count (the
+// e4m3 form issues in two thirds of its slots), so the arithmetic runs on pairs of
+// fp32 values.
 #pragma once
 
 #include "common.cuh"
@@ -49,6 +51,65 @@ struct f8 {
     float v[8];
 };
 
+// Two fp32 values in a register pair: one instruction for both, each rounded as the
+// scalar operation rounds.  With scalar operations the gradient of T=4099 d=7168 took
+// 44.7 us against 42.1, the forward pass 1 to 3% longer.
+using f2 = unsigned long long;
+
+__device__ __forceinline__ f2 f2_of(float lo, float hi)
+{
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ float2 f2_get(f2 a)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c)
+{
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b)
+{
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b)
+{
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The two bf16 values of a word, and back.
+__device__ __forceinline__ f2 f2_bf16(uint32_t w)
+{
+    return f2_of(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ uint32_t f2_pack(f2 a)
+{
+    const float2 v = f2_get(a);
+    const __nv_bfloat162 p = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+struct w4 {
+    uint32_t w[4];
+};
+
+__device__ __forceinline__ w4 words(const uint4& u) { return w4{{u.x, u.y, u.z, u.w}}; }
+
 __device__ __forceinline__ f8 unpack8(const uint4& u)
 {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -71,6 +132,43 @@ __device__ __forceinline__ uint4 pack8(const f8& f)
         w[i] = *reinterpret_cast<const uint32_t*>(&p);
     }
     return u;
+}
+
+// bf16(a + b), the sum of the squares of a (four in each half, then the halves),
+// and bf16((a w)(r0 + r1)), eight values at a time.
+__device__ __forceinline__ uint4 add_bf16x8(const uint4& a, const uint4& b)
+{
+    const w4 x = words(a), y = words(b);
+    w4 o;
+#pragma unroll
+    for (int j = 0; j < 4; j++) o.w[j] = f2_pack(f2_add(f2_bf16(x.w[j]), f2_bf16(y.w[j])));
+    return make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
+}
+
+__device__ __forceinline__ float squares8(const uint4& a)
+{
+    const w4 x = words(a);
+    f2 q = f2_mul(f2_bf16(x.w[0]), f2_bf16(x.w[0]));
+#pragma unroll
+    for (int j = 1; j < 4; j++) {
+        const f2 v = f2_bf16(x.w[j]);
+        q = f2_fma(v, v, q);
+    }
+    const float2 h = f2_get(q);
+    return h.x + h.y;
+}
+
+__device__ __forceinline__ uint4 scale_bf16x8(const uint4& a, const uint4& w, float r0, float r1)
+{
+    const w4 x = words(a), y = words(w);
+    const f2 p0 = f2_of(r0, r0), p1 = f2_of(r1, r1);
+    w4 o;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const f2 sw = f2_mul(f2_bf16(x.w[j]), f2_bf16(y.w[j]));
+        o.w[j] = f2_pack(f2_fma(sw, p0, f2_mul(sw, p1)));
+    }
+    return make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
 }
 
 // 16 bf16 values: 32 bytes, one load or store where the address allows it.  With
@@ -279,15 +377,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a, int war
 #pragma unroll
         for (int i = 0; i < WPT; i++) {
             const int v = i * gt + ti;
-            f8 s = unpack8(u[i].lo), t = unpack8(r[i].lo);
-#pragma unroll
-            for (int j = 0; j < 8; j++) s.v[j] += t.v[j];
-            u[i].lo = pack8(s);
-            s = unpack8(u[i].hi);
-            t = unpack8(r[i].hi);
-#pragma unroll
-            for (int j = 0; j < 8; j++) s.v[j] += t.v[j];
-            u[i].hi = pack8(s);
+            u[i].lo = add_bf16x8(u[i].lo, r[i].lo);
+            u[i].hi = add_bf16x8(u[i].hi, r[i].hi);
             if (v < nw) store16(a.xsum + base + 16 * v, u[i], a.al32);
         }
     }
@@ -295,17 +386,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a, int war
         double ss = 0.0;
 #pragma unroll
         for (int i = 0; i < WPT; i++) {
-            const f8 s = unpack8(u[i].lo), t = unpack8(u[i].hi);
-            float p = 0.f, q = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                p = fmaf(s.v[j], s.v[j], p);
-                q = fmaf(t.v[j], t.v[j], q);
-            }
-            ss += (double)p + (double)q;
+            ss += (double)squares8(u[i].lo) + (double)squares8(u[i].hi);
         }
         ss = group_sum(ss, s_sum + group * warps, group, warps);
-        // Squares of bf16 values are exact; eight at a time add up in fp32 and the rest, the
+        // Squares of bf16 values are exact; eight at a time add up in fp32, and their sums, the
         // mean and eps in 64 bits.  1 / sqrt(var) is r0 + r1: r0 from rsqrtf (within 2 units
         // in the last place), r1 one Newton step from its residual 1 - var r0^2.  s * w is
         // exact too, so y is (s w)(r0 + r1) with one rounding to fp32 before the one to bf16:
@@ -320,21 +404,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a, int war
             const int v = i * gt + ti;
             if (v < nw) {
                 const v16 wv = load16(a.weight + 16 * v, a.al32);
-                f8 s = unpack8(u[i].lo), w = unpack8(wv.lo);
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const float sw = s.v[j] * w.v[j];
-                    s.v[j] = fmaf(sw, r0, sw * r1);
-                }
-                u[i].lo = pack8(s);
-                s = unpack8(u[i].hi);
-                w = unpack8(wv.hi);
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const float sw = s.v[j] * w.v[j];
-                    s.v[j] = fmaf(sw, r0, sw * r1);
-                }
-                u[i].hi = pack8(s);
+                u[i].lo = scale_bf16x8(u[i].lo, wv.lo, r0, r1);
+                u[i].hi = scale_bf16x8(u[i].hi, wv.hi, r0, r1);
                 if (OUT == NORM_BF16 || a.y) store16(a.y + base + 16 * v, u[i], a.al32);
             }
         }
@@ -394,9 +465,10 @@ struct NormGradArgs {
 // so that a row takes at most 512 threads up to d = 16384 and a thread may hold
 // 128 registers (its columns' dw are 8 a vector).  Wider rows take 1024 threads
 // of 64 registers, which then read the weight again for every row.  Measured
-// (T=4099): d=7168 44.7 us with 4 vectors, 48.7 with 2, 66.7 with 1 -- the sums
-// over a row cost every warp the same, so few warps with much of the row each
-// are better -- and d=2048 17.4 with 2, 20.2 with 4, where a row is short.
+// (T=4099, scalar arithmetic): d=7168 44.7 us with 4 vectors, 48.7 with 2, 66.7
+// with 1 -- the sums over a row cost every warp the same, so few warps with much
+// of the row each are better -- and d=2048 17.4 with 2, 20.2 with 4, where a row
+// is short.
 __host__ __device__ inline RowShape norm_grad_shape(int d) { return row_shape(d / 8, d <= 4096 ? 2 : 4); }
 
 // Rows in flight a group: every thread copies its own vectors of s, dy and dxsum
@@ -449,13 +521,13 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_grad_kernel(const NormGradArgs a
         const int v = i * gt + ti;
         return v < nvec ? __ldg(reinterpret_cast<const uint4*>(a.weight) + v) : make_uint4(0u, 0u, 0u, 0u);
     };
-    float dw[VPT][8];
+    f2 dw[VPT][4];
     uint4 w[kKeepW ? VPT : 1];
 #pragma unroll
     for (int i = 0; i < VPT; i++) {
         if (kKeepW) w[i] = weight(i);
 #pragma unroll
-        for (int j = 0; j < 8; j++) dw[i][j] = 0.f;
+        for (int j = 0; j < 4; j++) dw[i][j] = f2_of(0.f, 0.f);
     }
     auto fetch = [&](int64_t row, int st) {
         if (row < a.T) {
@@ -480,17 +552,20 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_grad_kernel(const NormGradArgs a
         ptx::cp_async_wait(stages - 1);
         const uint4* mine = slots + st * 3 * VPT * nt;
         if (++st == stages) st = 0;
-        float ss = 0.f, dot = 0.f;
+        f2 ss2 = f2_of(0.f, 0.f), dot2 = f2_of(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < VPT; i++) {
             if (i * gt + ti >= nvec) continue;
-            const f8 s = unpack8(mine[i * nt]), g = unpack8(mine[(VPT + i) * nt]), wf = unpack8(kKeepW ? w[i] : weight(i));
+            const w4 s = words(mine[i * nt]), g = words(mine[(VPT + i) * nt]), wf = words(kKeepW ? w[i] : weight(i));
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                ss = fmaf(s.v[j], s.v[j], ss);
-                dot = fmaf(g.v[j] * wf.v[j], s.v[j], dot);
+            for (int j = 0; j < 4; j++) {
+                const f2 sv = f2_bf16(s.w[j]);
+                ss2 = f2_fma(sv, sv, ss2);
+                dot2 = f2_fma(f2_mul(f2_bf16(g.w[j]), f2_bf16(wf.w[j])), sv, dot2);
             }
         }
+        const float2 sp = f2_get(ss2), dp = f2_get(dot2);
+        float ss = sp.x + sp.y, dot = dp.x + dp.y;
         // both sums through one barrier; the scratch alternates from row to row
         ss = warp_sum(ss);
         dot = warp_sum(dot);
@@ -506,24 +581,22 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_grad_kernel(const NormGradArgs a
         }
         const float rstd = rsqrtf(ss / (float)a.d + a.eps);
         const float m = dot * rstd / (float)a.d;      // mean(g * n)
+        const f2 rstd2 = f2_of(rstd, rstd), mneg2 = f2_of(-m, -m);
 #pragma unroll
         for (int i = 0; i < VPT; i++) {
             const int v = i * gt + ti;
             if (v >= nvec) continue;
-            const f8 s = unpack8(mine[i * nt]), g = unpack8(mine[(VPT + i) * nt]), wf = unpack8(kKeepW ? w[i] : weight(i));
-            f8 o;
+            const w4 s = words(mine[i * nt]), g = words(mine[(VPT + i) * nt]), wf = words(kKeepW ? w[i] : weight(i));
+            w4 r{{0u, 0u, 0u, 0u}}, o;
+            if (a.dxsum) r = words(mine[(2 * VPT + i) * nt]);
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const float n = s.v[j] * rstd;
-                o.v[j] = (g.v[j] * wf.v[j] - n * m) * rstd;
-                dw[i][j] = fmaf(g.v[j], n, dw[i][j]);
+            for (int j = 0; j < 4; j++) {
+                const f2 gv = f2_bf16(g.w[j]), n = f2_mul(f2_bf16(s.w[j]), rstd2);
+                const f2 t = f2_fma(n, mneg2, f2_mul(gv, f2_bf16(wf.w[j])));
+                o.w[j] = f2_pack(f2_fma(t, rstd2, f2_bf16(r.w[j])));
+                dw[i][j] = f2_fma(gv, n, dw[i][j]);
             }
-            if (a.dxsum) {
-                const f8 r = unpack8(mine[(2 * VPT + i) * nt]);
-#pragma unroll
-                for (int j = 0; j < 8; j++) o.v[j] += r.v[j];
-            }
-            reinterpret_cast<uint4*>(a.dx + row * a.d)[v] = pack8(o);
+            reinterpret_cast<uint4*>(a.dx + row * a.d)[v] = make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
         }
     }
     ptx::cp_async_wait(0);
@@ -539,9 +612,10 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_grad_kernel(const NormGradArgs a
                 const int v = i * gt + ti;
                 if (v >= nvec) continue;
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    if (g > 0) dw[i][j] += sum[8 * v + j];
-                    sum[8 * v + j] = dw[i][j];
+                for (int j = 0; j < 4; j++) {
+                    f2* at = reinterpret_cast<f2*>(sum) + 4 * v + j;
+                    if (g > 0) dw[i][j] = f2_add(dw[i][j], *at);
+                    *at = dw[i][j];
                 }
             }
         }
@@ -551,9 +625,9 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_grad_kernel(const NormGradArgs a
     for (int i = 0; i < VPT; i++) {
         const int v = i * gt + ti;
         if (v < nvec) {
-            float4* p = reinterpret_cast<float4*>(part) + 2 * v;
-            p[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-            p[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+            ulonglong2* p = reinterpret_cast<ulonglong2*>(part) + 2 * v;
+            p[0] = make_ulonglong2(dw[i][0], dw[i][1]);
+            p[1] = make_ulonglong2(dw[i][2], dw[i][3]);
         }
     }
 }
