@@ -129,6 +129,21 @@ __device__ __forceinline__ I8Tile i8_tile(int t, const Int8Args& a, const I8Plan
     return tl;
 }
 
+// Rows of B that the CTA of this rank loads for a tile: its share of the tile's
+// rows, whole 64s and 16s and a last box for the rest.  The rest of a dense product
+// is always T % 16 rows, a box of that height; an expert's is brought in a box of 4,
+// 8 or 16 (the rows behind it are other experts', or zeros past the last row).
+// Rows that no box brings stay as they are in shared memory: they only reach columns
+// that are not stored.  Rows cost time even where they are few, and boxes that lie
+// mostly past the last row cost more: with 16-row boxes throughout, K=2048 N=108544
+// took 43 us at T=4 and 45 at T=17 against 39 at T=16; now 37, 39 and 39.
+__device__ __forceinline__ int i8_rows_loaded(const Int8Args& a, const I8Tile& tl, int rank)
+{
+    const int rows = min(tl.b_n, max(0, tl.rows - rank * tl.b_n)), rest = rows & 15;
+    if (!a.counts || rest == 0) return rows;
+    return (rows & ~15) + (rest <= 4 ? 4 : rest <= 8 ? 8 : 16);
+}
+
 // Builds the plan of a grouped product (every thread of the CTA).  Returns false
 // when a segment lies outside the rows.  slots: CTAs (or pairs) of the launch.
 //
@@ -138,25 +153,49 @@ __device__ __forceinline__ I8Tile i8_tile(int t, const Int8Args& a, const I8Plan
 // busy.  A block of n rows is cut into ceil(n / cap) units of equal width.
 __device__ __forceinline__ bool i8_plan(const Int8Args& a, I8Plan* p, int mt, int nk, int slots, bool pair)
 {
+    constexpr int kMine = (kMaxExperts + kI8Threads - 1) / kI8Threads;   // experts a thread takes
     const int tid = threadIdx.x, lane = tid & 31;
     const int align = pair ? 32 : 16;
+    int n[kMine], o[kMine], rank[kMine];
     bool bad = false;
-    for (int e = tid; e < a.E; e += kI8Threads) {
-        const int n = a.counts[e], o = a.offsets[e];
-        bad |= n < 0 || n > a.T || (n > 0 && (o < 0 || o > a.T - n));
-        p->n[e] = n;
+#pragma unroll
+    for (int i = 0; i < kMine; i++) {
+        const int e = tid + i * kI8Threads;
+        n[i] = e < a.E ? a.counts[e] : 0;
+        o[i] = e < a.E ? a.offsets[e] : 0;
     }
-    if (tid < ((-a.E) & 3)) p->n[a.E + tid] = 0;
+#pragma unroll
+    for (int i = 0; i < kMine; i++) {
+        const int e = tid + i * kI8Threads;
+        bad |= n[i] < 0 || n[i] > a.T || (n[i] > 0 && (o[i] < 0 || o[i] > a.T - n[i]));
+        if (e < ((a.E + 3) & ~3)) p->n[e] = n[i];
+    }
     if (__syncthreads_or(bad)) return false;
+#pragma unroll
+    for (int i = 0; i < kMine; i++) {
+        const int e = tid + i * kI8Threads;
+        int r = 0;      // more rows first, then the lower expert
+        if (n[i] > 0) {
+#pragma unroll 4
+            for (int j = 0; j < a.E; j += 4) {
+                const int4 m = *reinterpret_cast<const int4*>(p->n + j);
+                r += m.x > n[i] || (m.x == n[i] && j < e);
+                r += m.y > n[i] || (m.y == n[i] && j + 1 < e);
+                r += m.z > n[i] || (m.z == n[i] && j + 2 < e);
+                r += m.w > n[i] || (m.w == n[i] && j + 3 < e);
+            }
+        }
+        rank[i] = r;
+    }
     if (tid < 32) {
         // total units under each cap, and the widest segment
         int u[4] = {0, 0, 0, 0}, most = 0, nb = 0;
         for (int e = lane; e < a.E; e += 32) {
-            const int n = p->n[e];
+            const int m = p->n[e];
 #pragma unroll
-            for (int i = 0; i < 4; i++) u[i] += (n + (256 >> i) - 1) / (256 >> i);
-            most = max(most, n);
-            nb += n > 0;
+            for (int i = 0; i < 4; i++) u[i] += (m + (256 >> i) - 1) / (256 >> i);
+            most = max(most, m);
+            nb += m > 0;
         }
         most = __reduce_max_sync(0xffffffffu, most);
         float least = 0.f;
@@ -181,22 +220,13 @@ __device__ __forceinline__ bool i8_plan(const Int8Args& a, I8Plan* p, int mt, in
     }
     __syncthreads();
     const int cap = p->cap;
-    for (int e = tid; e < a.E; e += kI8Threads) {
-        const int n = p->n[e];
-        if (n == 0) continue;
-        int r = 0;      // rank: more rows first, then the lower expert
-#pragma unroll 4
-        for (int j = 0; j < a.E; j += 4) {
-            const int4 m = *reinterpret_cast<const int4*>(p->n + j);
-            r += m.x > n || (m.x == n && j < e);
-            r += m.y > n || (m.y == n && j + 1 < e);
-            r += m.z > n || (m.z == n && j + 2 < e);
-            r += m.w > n || (m.w == n && j + 3 < e);
-        }
-        const int units = (n + cap - 1) / cap;
-        const int chunk = ((n + units - 1) / units + align - 1) / align * align;
-        p->blk[r] = make_int4(e, a.offsets[e], n, chunk);
-        p->units[r] = units;
+#pragma unroll
+    for (int i = 0; i < kMine; i++) {
+        if (n[i] == 0) continue;
+        const int units = (n[i] + cap - 1) / cap;
+        const int chunk = ((n[i] + units - 1) / units + align - 1) / align * align;
+        p->blk[rank[i]] = make_int4(tid + i * kI8Threads, o[i], n[i], chunk);
+        p->units[rank[i]] = units;
     }
     __syncthreads();
     if (tid < 32) {
@@ -258,8 +288,11 @@ __device__ __forceinline__ void i8_turn16(const uint32_t (&w)[8], uint4 (&o)[2],
 template <int FORM>
 __global__ void __launch_bounds__(kI8Threads, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB16,
-                     const __grid_constant__ CUtensorMap mB64, const Int8Args a)
+                     const __grid_constant__ CUtensorMap mB64, const __grid_constant__ CUtensorMap mB4,
+                     const __grid_constant__ CUtensorMap mB8, const Int8Args a)
 {
+    // mA: 128 channels a box; mB64, mB16: 64 and 16 rows; the rest: grouped mB8 and mB4,
+    // of 8 and 4 rows, dense mB4, of T % 16 rows
     constexpr bool PAIR = FORM == I8_PAIR;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -342,7 +375,11 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             for (int t = first; ok && t < total; t += step) {
                 const I8Tile tl = i8_tile<FORM>(t, a, splan, rank);
                 const int a_row = tl.e * a.N + tl.ma * 128;
-                const uint32_t tx = (PAIR ? 2u : 1u) * (kATileBytes + (uint32_t)tl.b_n * kBRowBytes);
+                const int rows = i8_rows_loaded(a, tl, PAIR ? rank : 0), rest = rows & 15;
+                // the leader of a pair counts both CTAs' bytes
+                const int all_rows = PAIR ? i8_rows_loaded(a, tl, 0) + i8_rows_loaded(a, tl, 1) : rows;
+                const uint32_t tx = (PAIR ? 2u : 1u) * kATileBytes + (uint32_t)all_rows * kBRowBytes;
+                const CUtensorMap* last = a.counts && rest == 8 ? &mB8 : &mB4;
                 for (int kb = kb0; kb < kb1; kb++) {
                     if (!bounded_wait(ptx::smem_u32(&ctl->empty[s]), ph ^ 1u, ctl, a.err)) {
                         ok = false;
@@ -358,11 +395,12 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                     const int kc = kb * kI8BlockK;
                     tma_load<PAIR>(a_dst, &mA, full, kc, a_row, pol);
                     const uint32_t b_dst = a_dst + kATileBytes;
-                    const int n64 = tl.b_n >> 6;
-                    for (int i = 0; i < n64; i++)
-                        tma_load<PAIR>(b_dst + i * 64 * kBRowBytes, &mB64, full, kc, tl.b_row0 + 64 * i, pol);
-                    for (int r = n64 * 64; r < tl.b_n; r += 16)
+                    int r = 0;
+                    for (; r + 64 <= rows; r += 64)
+                        tma_load<PAIR>(b_dst + r * kBRowBytes, &mB64, full, kc, tl.b_row0 + r, pol);
+                    for (; r + 16 <= rows; r += 16)
                         tma_load<PAIR>(b_dst + r * kBRowBytes, &mB16, full, kc, tl.b_row0 + r, pol);
+                    if (rest) tma_load<PAIR>(b_dst + r * kBRowBytes, last, full, kc, tl.b_row0 + r, pol);
                     if (++s == stages) {
                         s = 0;
                         ph ^= 1u;

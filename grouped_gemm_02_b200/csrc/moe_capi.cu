@@ -1446,20 +1446,25 @@ int norm_entry(const moe_bf16* x, const moe_bf16* residual, const moe_bf16* weig
 int run_int8(const Int8Args& a, const void* xq, int64_t rows, const void* Wq, int64_t wrows, int form, int64_t tiles,
              int split, const DeviceState* dev, cudaStream_t st)
 {
-    CUtensorMap ma, mb16, mb64;
+    CUtensorMap ma, mb16, mb64, mb4, mb8;
     if (!make_map_u8(&ma, Wq, a.K, wrows, 128) || !make_map_u8(&mb16, xq, a.K, rows, 16) ||
         !make_map_u8(&mb64, xq, a.K, rows, 64))
         return MOE_ERR_CUDA;
+    // the rows behind the last whole 16 of a tile: T % 16 of a dense product, 4 or 8 of an expert
+    const uint32_t rest = a.counts ? 4 : rows % 16 != 0 ? (uint32_t)(rows % 16) : 16;
+    if (!make_map_u8(&mb4, xq, a.K, rows, rest)) return MOE_ERR_CUDA;
+    mb8 = mb4;
+    if (a.counts && !make_map_u8(&mb8, xq, a.K, rows, 8)) return MOE_ERR_CUDA;
     const dim3 block(kI8Threads);
     if (form == I8_PAIR)
         return status_of(launch_cluster(int8_gemm_kernel<I8_PAIR>, 2,
                                         dim3((unsigned)(2 * std::min<int64_t>(tiles, dev->i8.pairs))), block,
-                                        kI8SmemBytes, st, ma, mb16, mb64, a));
+                                        kI8SmemBytes, st, ma, mb16, mb64, mb4, mb8, a));
     if (form == I8_SPLIT)
         return status_of(launch_cluster(int8_gemm_kernel<I8_SPLIT>, split, dim3((unsigned)tiles * split), block,
-                                        kI8SmemBytes, st, ma, mb16, mb64, a));
+                                        kI8SmemBytes, st, ma, mb16, mb64, mb4, mb8, a));
     return status_of(launch(int8_gemm_kernel<I8_SINGLE>, dim3((unsigned)std::min<int64_t>(tiles, dev->sm_count)),
-                            block, kI8SmemBytes, st, ma, mb16, mb64, a));
+                            block, kI8SmemBytes, st, ma, mb16, mb64, mb4, mb8, a));
 }
 
 int check_int8(int64_t N, int64_t K)
