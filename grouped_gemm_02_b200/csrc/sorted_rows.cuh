@@ -231,105 +231,134 @@ __global__ void __launch_bounds__(kSortChunk) sort_small_kernel(const int32_t* _
 }
 
 // ---------------------------------------------------------------- back, and the gradient of sort
-// out[t] = sum_j w[t, j] rows[pos] + add[t]; w null: weights 1.  One thread per
-// 16-byte vector of a token's row, its k loads in flight together.
-__global__ void __launch_bounds__(256) return_rows_kernel(const bf16* __restrict__ rows,
-                                                          const int32_t* __restrict__ inv_perm,
-                                                          const float* __restrict__ gates, const bf16* __restrict__ add,
-                                                          int64_t T, int k, int d, bf16* __restrict__ out)
+// out[t] = sum_j w[t, j] rows[pos] + add[t]; w null: weights 1.  k <= KM, and a
+// thread takes V = 8 / KM vectors of a token's row, so that eight loads of 16 bytes
+// are in flight together whatever k is (with one vector a thread k = 1 reached 30%
+// of the bytes that k = 8 did: T=4093 d=7168 60 us against 17).  BRIEF: short rows, a
+// warp a token and four tokens a CTA; otherwise a CTA has one token, whose positions
+// and gates are then the same registers for every thread.
+template <int KM, bool BRIEF>
+__global__ void __launch_bounds__(BRIEF ? 128 : 64) return_rows_kernel(const bf16* __restrict__ rows,
+                                                         const int32_t* __restrict__ inv_perm,
+                                                         const float* __restrict__ gates, const bf16* __restrict__ add,
+                                                         int64_t T, int k, int d, bf16* __restrict__ out)
 {
+    constexpr int V = kMaxTopK / KM;
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     const int nvec = d / 8;
     const int64_t P = T * k;
-    const int64_t t = blockIdx.x;
-    int pos[kMaxTopK];
-    float w[kMaxTopK];
+    const int64_t t = BRIEF ? (int64_t)blockIdx.x * blockDim.y + threadIdx.y : blockIdx.x;
+    if (BRIEF && t >= T) return;
+    int pos[KM];
+    float w[KM];
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; j++) {
+    for (int j = 0; j < KM; j++) {
         pos[j] = j < k ? pair_pos(inv_perm, t * k + j, P) : -1;
         w[j] = (j < k && gates) ? __ldg(gates + t * k + j) : 1.f;
     }
-    for (int v = blockIdx.y * blockDim.x + threadIdx.x; v < nvec; v += gridDim.y * blockDim.x) {
-        uint4 u[kMaxTopK];
+    const int v0 = blockIdx.y * (blockDim.x * V) + threadIdx.x;
+    uint4 u[V][KM];
 #pragma unroll
-        for (int j = 0; j < kMaxTopK; j++)
-            if (pos[j] >= 0) u[j] = __ldg(reinterpret_cast<const uint4*>(rows + (int64_t)pos[j] * d) + v);
+    for (int i = 0; i < V; i++)
+#pragma unroll
+        for (int j = 0; j < KM; j++)
+            if (pos[j] >= 0 && v0 + i * (int)blockDim.x < nvec)
+                u[i][j] = __ldg(reinterpret_cast<const uint4*>(rows + (int64_t)pos[j] * d) + v0 + i * blockDim.x);
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+        const int v = v0 + i * blockDim.x;
+        if (v >= nvec) continue;
         f8 acc;
 #pragma unroll
-        for (int i = 0; i < 8; i++) acc.v[i] = 0.f;
+        for (int c = 0; c < 8; c++) acc.v[c] = 0.f;
 #pragma unroll
-        for (int j = 0; j < kMaxTopK; j++) {
+        for (int j = 0; j < KM; j++) {
             if (pos[j] >= 0) {
-                const f8 r = unpack8(u[j]);
+                const f8 r = unpack8(u[i][j]);
 #pragma unroll
-                for (int i = 0; i < 8; i++) acc.v[i] = fmaf(w[j], r.v[i], acc.v[i]);
+                for (int c = 0; c < 8; c++) acc.v[c] = fmaf(w[j], r.v[c], acc.v[c]);
             }
         }
         if (add) {
-            const f8 r = unpack8(__ldg(reinterpret_cast<const uint4*>(add + t * d) + v));
+            const f8 r = unpack8(reinterpret_cast<const uint4*>(add + t * d)[v]);
 #pragma unroll
-            for (int i = 0; i < 8; i++) acc.v[i] += r.v[i];
+            for (int c = 0; c < 8; c++) acc.v[c] += r.v[c];
         }
         reinterpret_cast<uint4*>(out + t * d)[v] = pack8(acc);
     }
 }
 
 // ---------------------------------------------------------------- gradient of back
-// One CTA per token: its threads hold the token's gradient row a vector at a
-// time, write each pair's scaled copy and add up the k dot products.
+// The threads of a token hold V = 8 / KM vectors of its gradient row at a time, write
+// each pair's scaled copy and add up the k dot products.  BRIEF: as above.
 // rows and drows may be the same buffer (no __restrict__, no read-only loads):
 // a vector is read and then written by the same thread.
-__global__ void __launch_bounds__(256) return_rows_grad_kernel(const bf16* __restrict__ dout, const bf16* rows,
-                                                               const int32_t* __restrict__ inv_perm,
-                                                               const float* __restrict__ gates, int64_t T, int k,
-                                                               int d, bf16* drows, float* __restrict__ dgates)
+template <int KM, int MAXT, bool BRIEF = false>
+__global__ void __launch_bounds__(MAXT)
+    return_rows_grad_kernel(const bf16* __restrict__ dout, const bf16* rows, const int32_t* __restrict__ inv_perm,
+                            const float* __restrict__ gates, int64_t T, int k, int d, bf16* drows,
+                            float* __restrict__ dgates)
 {
-    __shared__ float s_dot[kMaxTopK][8];
+    constexpr int V = kMaxTopK / KM;
+    __shared__ float s_dot[KM][MAXT / 32];
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    const int nvec = d / 8;
     const int64_t P = T * k;
-    const int64_t t = blockIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int pos[kMaxTopK];
-    float w[kMaxTopK], dot[kMaxTopK];
+    const int64_t t = BRIEF ? (int64_t)blockIdx.x * blockDim.y + threadIdx.y : blockIdx.x;
+    const int warps = (int)(blockDim.x >> 5), lane = threadIdx.x & 31;     // warps of a token
+    const int first = BRIEF ? threadIdx.y * warps : 0, warp = first + (int)(threadIdx.x >> 5);
+    const bool live = !BRIEF || t < T;
+    const int nvec = live ? d / 8 : 0;
+    int pos[KM];
+    float w[KM], dot[KM];
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; j++) {
-        pos[j] = j < k ? pair_pos(inv_perm, t * k + j, P) : -1;
-        w[j] = j < k ? __ldg(gates + t * k + j) : 0.f;
+    for (int j = 0; j < KM; j++) {
+        pos[j] = live && j < k ? pair_pos(inv_perm, t * k + j, P) : -1;
+        w[j] = live && j < k ? __ldg(gates + t * k + j) : 0.f;
         dot[j] = 0.f;
     }
-    for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
-        uint4 u[kMaxTopK];
+    for (int v0 = threadIdx.x; v0 < nvec; v0 += V * blockDim.x) {
+        uint4 u[V][KM], ug[V];
 #pragma unroll
-        for (int j = 0; j < kMaxTopK; j++)
-            if (pos[j] >= 0) u[j] = reinterpret_cast<const uint4*>(rows + (int64_t)pos[j] * d)[v];
-        const f8 g = unpack8(__ldg(reinterpret_cast<const uint4*>(dout + t * d) + v));
+        for (int i = 0; i < V; i++) {
+            const int v = v0 + i * blockDim.x;
+            if (V == 1 || v < nvec) {
 #pragma unroll
-        for (int j = 0; j < kMaxTopK; j++) {
-            if (pos[j] >= 0) {
-                const f8 r = unpack8(u[j]);
-                f8 o;
+                for (int j = 0; j < KM; j++)
+                    if (pos[j] >= 0) u[i][j] = reinterpret_cast<const uint4*>(rows + (int64_t)pos[j] * d)[v];
+                ug[i] = __ldg(reinterpret_cast<const uint4*>(dout + t * d) + v);
+            }
+        }
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    dot[j] = fmaf(g.v[i], r.v[i], dot[j]);
-                    o.v[i] = w[j] * g.v[i];
+        for (int i = 0; i < V; i++) {
+            const int v = v0 + i * blockDim.x;
+            if (V > 1 && v >= nvec) continue;
+            const f8 g = unpack8(ug[i]);
+#pragma unroll
+            for (int j = 0; j < KM; j++) {
+                if (pos[j] >= 0) {
+                    const f8 r = unpack8(u[i][j]);
+                    f8 o;
+#pragma unroll
+                    for (int c = 0; c < 8; c++) {
+                        dot[j] = fmaf(g.v[c], r.v[c], dot[j]);
+                        o.v[c] = w[j] * g.v[c];
+                    }
+                    reinterpret_cast<uint4*>(drows + (int64_t)pos[j] * d)[v] = pack8(o);
                 }
-                reinterpret_cast<uint4*>(drows + (int64_t)pos[j] * d)[v] = pack8(o);
             }
         }
     }
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; j++) {
+    for (int j = 0; j < KM; j++) {
         const float s = warp_sum(dot[j]);
         if (lane == 0) s_dot[j][warp] = s;
     }
     __syncthreads();
-    const int warps = (int)(blockDim.x >> 5);
-    if ((int)threadIdx.x < k) {
-        float s = s_dot[threadIdx.x][0];
-        for (int i = 1; i < warps; i++) s += s_dot[threadIdx.x][i];
+    if (live && (int)threadIdx.x < k) {
+        float s = s_dot[threadIdx.x][first];
+        for (int i = 1; i < warps; i++) s += s_dot[threadIdx.x][first + i];
         dgates[t * k + threadIdx.x] = s;
     }
 }

@@ -17,7 +17,8 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda"
 
 SIZES = [(1, 4, 1, 64), (1, 256, 8, 7168), (2, 2, 2, 192), (7, 8, 3, 1088), (32, 64, 8, 2048), (128, 8, 8, 64),
-         (129, 8, 8, 320), (333, 384, 8, 448), (700, 16, 5, 4096), (2049, 512, 2, 128), (3, 3, 1, 16384)]
+         (129, 8, 8, 320), (333, 384, 8, 448), (700, 16, 5, 4096), (2049, 512, 2, 128), (3, 3, 1, 16384),
+         (301, 8, 1, 7168), (299, 8, 2, 4096), (303, 4, 4, 2112), (777, 8, 1, 64), (402, 8, 3, 256), (1023, 8, 8, 256)]
 
 
 def _routing(T, E, k, seed, bad=()):
