@@ -448,7 +448,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a, int war
 // rstd is formed again from s, which is read anyway.  Each group walks the rows
 // group, group + groups, ... and keeps its columns' dw in registers; a CTA adds
 // its groups and writes one row of partials[CTA][d], and norm_dw_kernel adds the
-// CTAs, all in a fixed order: no atomics, the same bits in every run.
+// CTAs, all in a fixed order: no atomics, the same bits in every run.  A single
+// CTA writes its row to dweight itself.
 struct NormGradArgs {
     const bf16* dy;
     const bf16* s;

@@ -72,7 +72,7 @@ def test_norm_grad_refusals(L):
     assert _norm_grad(L, eps=0.0) == -1
     for name in ("dy", "xsum", "weight", "dx", "dweight", "ws"):
         assert _norm_grad(L, **{name: None}) == -1, name
-    for name in ("dy", "xsum", "weight", "dxsum", "dx", "ws"):
+    for name in ("dy", "xsum", "weight", "dxsum", "dx", "dweight", "ws"):
         assert _norm_grad(L, **{name: ODD}) == -2, name
     need = moe.moe_rmsnorm_backward_workspace_size(4, 256)
     assert _norm_grad(L, ws_bytes=need // 2) == -3
