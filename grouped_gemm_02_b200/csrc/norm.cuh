@@ -23,6 +23,7 @@
 
 #include "common.cuh"
 #include "fp8.cuh"
+#include "int8_code.h"
 #include "ptx.cuh"
 
 namespace moe {
@@ -259,30 +260,14 @@ __device__ __forceinline__ uint32_t amax_bits8(const uint4& u)
 }
 
 // ---------------------------------------------------------------- int8 codes
-// One scale a row: scale = amax / 127, code = round(v * (127 / amax)) to even.
-// A row whose largest magnitude is below 2^-100 counts as all zero (scale 1,
-// codes 0): amax / 127 and 127 / amax are then both normal fp32 numbers.  A row
-// that holds a NaN or an infinity gets the scale NaN, so that it stays visible
-// in every product made of it.
-struct Int8Scale {
-    float scale, inv;
-};
-
-__device__ __forceinline__ Int8Scale int8_scale(uint32_t amax_bits)
-{
-    if (amax_bits >= 0x7F800000u) return {__uint_as_float(0x7FC00000u), 0.f};
-    const float amax = __uint_as_float(amax_bits);
-    if (amax < 7.888609052210118e-31f) return {1.f, 0.f};   // 2^-100
-    return {amax / 127.f, 127.f / amax};
-}
-
+// One scale a row (int8_code.h).
 __device__ __forceinline__ uint2 int8_codes8(const uint4& u, float inv)
 {
     const f8 f = unpack8(u);
     uint32_t w[2] = {0u, 0u};
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        // |v * inv| <= 127 (1 + 2^-23): rounds to at most 127.  inv = 0 (a NaN or
+        // |v * inv| <= 127 (1 + 2^-22): rounds to at most 127.  inv = 0 (a NaN or
         // infinite row) makes 0 or NaN, and a NaN converts to code 0.
         const int c = __float2int_rn(f.v[i] * inv);
         w[i >> 2] |= (uint32_t)(c & 0xFF) << (8 * (i & 3));

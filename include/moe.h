@@ -302,8 +302,8 @@ MOE_API int moe_rmsnorm_backward(const moe_bf16 *dy, const moe_bf16 *xsum, const
 
 /* ---------------------------------------------------------------- int8 products
  * 8-bit integer codes with one scale a row (a token, or a channel of a weight
- * matrix): scale = max|v| / 127, code = v * (127 / max|v|) rounded to nearest,
- * ties to even, in -127..127.  A row whose largest magnitude is below 2^-100
+ * matrix): scale = max|v| / 127 in fp32, code = v * 127 / max|v| rounded to
+ * nearest, ties to even, in -127..127.  A row whose largest magnitude is below 2^-100
  * counts as zero (scale 1).  A row that holds a NaN or an infinity gets the
  * scale NaN, so every product of it is NaN. */
 
