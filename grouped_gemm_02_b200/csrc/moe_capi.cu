@@ -1500,6 +1500,7 @@ int moe_rmsnorm_int8(const moe_bf16* x, const moe_bf16* residual, const moe_bf16
 int moe_rmsnorm_backward_workspace_size(int64_t T, int64_t d, size_t* bytes)
 {
     if (!bytes || T < 0 || T >= (int64_t(1) << 31) || d <= 0 || d > kNormMaxD) return MOE_ERR_ARG;
+    if (d % 64 != 0) return MOE_ERR_ALIGN;
     *bytes = align_up((size_t)norm_grad_ctas(T, (int)d) * d * 4, 256);
     return MOE_OK;
 }

@@ -284,7 +284,8 @@ MOE_API int moe_rmsnorm_fp8(const moe_bf16 *x, const moe_bf16 *residual, const m
 MOE_API int moe_rmsnorm_int8(const moe_bf16 *x, const moe_bf16 *residual, const moe_bf16 *weight, int64_t T, int64_t d,
                              float eps, moe_bf16 *xsum, moe_bf16 *y, int8_t *q, float *scale, void *stream);
 
-/* Workspace bytes of moe_rmsnorm_backward for these sizes (0 at T = 0). */
+/* Workspace bytes of moe_rmsnorm_backward for these sizes (0 at T = 0).  Sizes that
+ * moe_rmsnorm_backward refuses are refused here with the same status. */
 MOE_API int moe_rmsnorm_backward_workspace_size(int64_t T, int64_t d, size_t *bytes);
 
 /* The gradient of moe_rmsnorm.  With xsum = s, rstd = 1 / sqrt(mean(s^2) + eps),
