@@ -346,7 +346,8 @@ MOE_API int moe_permute_int8(const int32_t *topk_idx, const int8_t *xq, const fl
  * them; moe_grouped_gemm's y_p carries them already and goes to moe_combine):
  *   out[t,:] = bf16( sum_j topk_w[t,j] y_p[inv_perm[t*k+j], :] (+ shared_out[t,:]) )
  * in fp32, ascending j, no atomics.  inv_perm is moe_permute's (every position
- * at most once); a pair whose position lies outside [0, T*k) adds nothing. */
+ * at most once); a pair whose position lies outside [0, T*k) adds nothing.
+ * shared_out [T,d] (NULL: none) may be out itself. */
 MOE_API int moe_combine_weighted(const moe_bf16 *y_p, const int32_t *inv_perm, const float *topk_w,
                                  const moe_bf16 *shared_out, int64_t T, int64_t k, int64_t d, moe_bf16 *out,
                                  void *stream);
