@@ -567,13 +567,16 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 const int col = i >> 5, c4 = (i & 31) * 4;
                 const int ch = tl.ma * 128 + c4;
                 if (ch >= a.N) continue;       // N % 4 == 0: all four channels or none
-                int sum[4] = {0, 0, 0, 0};
+                int sum[4] = {0, 0, 0, 0}, gave_up = 0;
                 for (int p = 0; p < split; p++) {
                     int v[4];
                     ptx::ld_cluster_v4(ptx::mapa_shared(ring + (uint32_t)(col * 128 + c4) * 4u, p), v);
+                    gave_up |= ptx::ld_cluster_s32(ptx::mapa_shared(ptx::smem_u32(&ctl->abort), p));
 #pragma unroll
                     for (int j = 0; j < 4; j++) sum[j] += v[j];
                 }
+                // a CTA whose wait ran out left no sums: the tile stays as it was, as in the other forms
+                if (gave_up) continue;
                 const float sx = __ldg(a.sx + tl.row0 + col);
                 const float4 sw = __ldg(reinterpret_cast<const float4*>(a.sw + ch));
                 __nv_bfloat162 lo = __floats2bfloat162_rn((float)sum[0] * sw.x * sx, (float)sum[1] * sw.y * sx);

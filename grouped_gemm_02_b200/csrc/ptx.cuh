@@ -404,6 +404,14 @@ __device__ __forceinline__ void ld_cluster_v4(uint32_t cluster_addr, int (&v)[4]
                  : "memory");
 }
 
+// One 32-bit word of it.
+__device__ __forceinline__ int ld_cluster_s32(uint32_t cluster_addr)
+{
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
 // tcgen05.cp of a pair: each CTA's 32 x 128-bit rows at this shared offset go to
 // its own TMEM (four columns, repeated into the four lane quadrants).
 __device__ __forceinline__ void tmem_cp_32x128b_warpx4_pair(uint32_t taddr, uint64_t sdesc)
