@@ -145,7 +145,8 @@ __device__ __forceinline__ int i8_rows_loaded(const Int8Args& a, const I8Tile& t
 }
 
 // Builds the plan of a grouped product (every thread of the CTA).  Returns false
-// when a segment lies outside the rows.  slots: CTAs (or pairs) of the launch.
+// when a segment lies outside the rows, or the segments hold more rows than there
+// are (they overlap, and the prefix of units might pass 32 bits).  slots: CTAs (or pairs) of the launch.
 //
 // The rows of a tile: at most `cap`, the one of 256, 128, 64 and 32 that costs
 // the least by the terms of i8_cost (waves of tiles, each by its bytes at an
@@ -190,13 +191,18 @@ __device__ __forceinline__ bool i8_plan(const Int8Args& a, I8Plan* p, int mt, in
     if (tid < 32) {
         // total units under each cap, and the widest segment
         int u[4] = {0, 0, 0, 0}, most = 0, nb = 0;
+        int64_t all = 0;
         for (int e = lane; e < a.E; e += 32) {
             const int m = p->n[e];
 #pragma unroll
             for (int i = 0; i < 4; i++) u[i] += (m + (256 >> i) - 1) / (256 >> i);
             most = max(most, m);
             nb += m > 0;
+            all += m;
         }
+        // a lane's sum is below 2^35: its halves add up in 32 bits
+        all = (int64_t)__reduce_add_sync(0xffffffffu, (int)(all >> 16)) * 65536 +
+              __reduce_add_sync(0xffffffffu, (int)(all & 0xFFFF));
         most = __reduce_max_sync(0xffffffffu, most);
         float least = 0.f;
         int cap = 256;
@@ -214,12 +220,13 @@ __device__ __forceinline__ bool i8_plan(const Int8Args& a, I8Plan* p, int mt, in
         }
         nb = __reduce_add_sync(0xffffffffu, nb);
         if (lane == 0) {
-            p->cap = cap;
+            p->cap = all > a.T ? 0 : cap;
             p->nb = nb;
         }
     }
     __syncthreads();
     const int cap = p->cap;
+    if (cap == 0) return false;
 #pragma unroll
     for (int i = 0; i < kMine; i++) {
         if (n[i] == 0) continue;
@@ -344,7 +351,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     if (a.counts) {
         const bool ok = i8_plan(a, splan, mt, nk, step, PAIR);
         if (!ok && threadIdx.x == 0) atomicOr(a.err, DEVERR_PLAN);
-        // segments outside the rows: every CTA sees the same counts and takes no tile
+        // segments that do not fit the rows: every CTA sees the same counts and takes no tile
         total = ok ? splan->tb[splan->nb] * mt : 0;
         widest = ok ? splan->widest : 32;
     }

@@ -326,7 +326,8 @@ MOE_API int moe_gemm_int8(const int8_t *xq, const float *sx, const int8_t *Wq, c
  * * sxp[r] * sw[e,n] ).  xpq [T*k,K], sxp [T*k], counts [E] and offsets [E+1] as
  * moe_permute_int8 leaves them, Wq [E,N,K], sw [E,N], out [T*k,N]; E*N < 2^31.
  * Rows past offsets[E] are left untouched.  `ws` is moe_gemm_int8's.  A segment
- * outside the T*k rows sets MOE_DEVERR_PLAN and nothing is computed. */
+ * outside the T*k rows, or segments of more than T*k rows in all, set
+ * MOE_DEVERR_PLAN and nothing is computed. */
 MOE_API int moe_grouped_gemm_int8(const int8_t *xpq, const float *sxp, const int32_t *counts, const int32_t *offsets,
                                   const int8_t *Wq, const float *sw, int64_t T, int64_t K, int64_t N, int64_t E,
                                   int64_t k, moe_bf16 *out, void *ws, size_t ws_bytes, void *stream);
