@@ -14,8 +14,8 @@
 //
 // Bound: HBM.  Every input is read once and every output written once: a row
 // stays in the registers of one group of warps between the reduction and the
-// normalisation.  T=16384 d=7168 with a residual on one B200: bf16 138 us (6.8
-// TB/s), e4m3 133 us (6.2 TB/s), int8 136 us (6.0 TB/s); the gradient at T=4099
+// normalisation.  T=16384 d=7168 with a residual on one B200: bf16 137 us (6.9
+// TB/s), e4m3 131 us (6.3 TB/s), int8 133 us (6.2 TB/s); the gradient at T=4099
 // d=7168 42 us (5.6 TB/s).  Next to the bytes it is the instructions that count (the
 // e4m3 form issues in two thirds of its slots), so the arithmetic runs on pairs of
 // fp32 values.
@@ -29,6 +29,7 @@
 namespace moe {
 
 constexpr int kNormMaxD = 32768;             // 1024 threads x 32 values
+constexpr int kDoubleInf = 0x7FF00000, kDoubleLow = (1023 - 50) << 20;   // high words of infinity and of 2^-50
 constexpr int NORM_BF16 = 0, NORM_FP8 = 1, NORM_INT8 = 2;
 
 // How rows are laid over a CTA: a row belongs to a group of `warps` warps whose
@@ -135,8 +136,8 @@ __device__ __forceinline__ uint4 pack8(const f8& f)
     return u;
 }
 
-// bf16(a + b), the sum of the squares of a (four in each half, then the halves),
-// and bf16((a w)(r0 + r1)), eight values at a time.
+// bf16(a + b), the sum of the squares of a or of c a (four in each half, then the
+// halves), and bf16(((p a) w)(r0 + r1)), eight values at a time.
 __device__ __forceinline__ uint4 add_bf16x8(const uint4& a, const uint4& b)
 {
     const w4 x = words(a), y = words(b);
@@ -159,14 +160,28 @@ __device__ __forceinline__ float squares8(const uint4& a)
     return h.x + h.y;
 }
 
-__device__ __forceinline__ uint4 scale_bf16x8(const uint4& a, const uint4& w, float r0, float r1)
+__device__ __forceinline__ float squares8(const uint4& a, float c)
+{
+    const w4 x = words(a);
+    const f2 cc = f2_of(c, c);
+    f2 q = f2_of(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const f2 v = f2_mul(f2_bf16(x.w[j]), cc);
+        q = f2_fma(v, v, q);
+    }
+    const float2 h = f2_get(q);
+    return h.x + h.y;
+}
+
+__device__ __forceinline__ uint4 scale_bf16x8(const uint4& a, const uint4& w, float p, float r0, float r1)
 {
     const w4 x = words(a), y = words(w);
-    const f2 p0 = f2_of(r0, r0), p1 = f2_of(r1, r1);
+    const f2 pp = f2_of(p, p), p0 = f2_of(r0, r0), p1 = f2_of(r1, r1);
     w4 o;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-        const f2 sw = f2_mul(f2_bf16(x.w[j]), f2_bf16(y.w[j]));
+        const f2 sw = f2_mul(f2_mul(f2_bf16(x.w[j]), pp), f2_bf16(y.w[j]));
         o.w[j] = f2_pack(f2_fma(sw, p0, f2_mul(sw, p1)));
     }
     return make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
@@ -335,7 +350,7 @@ struct NormArgs {
 template <int OUT, int WPT>
 __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a, int warps)
 {
-    __shared__ double s_sum[32];
+    __shared__ double s_sum[2][32];
     __shared__ uint32_t s_max[32];
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
@@ -373,24 +388,52 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a, int war
         for (int i = 0; i < WPT; i++) {
             ss += (double)squares8(u[i].lo) + (double)squares8(u[i].hi);
         }
-        ss = group_sum(ss, s_sum + group * warps, group, warps);
-        // Squares of bf16 values are exact; eight at a time add up in fp32, and their sums, the
-        // mean and eps in 64 bits.  1 / sqrt(var) is r0 + r1: r0 from rsqrtf (within 2 units
-        // in the last place), r1 one Newton step from its residual 1 - var r0^2.  s * w is
-        // exact too, so y is (s w)(r0 + r1) with one rounding to fp32 before the one to bf16:
-        // a y whose last place differs from the definition's can flip a code.
+        ss = group_sum(ss, s_sum[0] + group * warps, group, warps);
+        // Squares of bf16 values are exact in fp32 between 2^-63 and 2^64; eight at a time
+        // add up there, and their sums, the mean and eps in 64 bits.  Where a square was
+        // beyond fp32 the sum is infinite; where all were below it and eps is so small that
+        // they count, it is tiny: such a row (the same for its whole group) is summed again
+        // with its values scaled by a power of two.  They are read again: kept for this in
+        // registers they cost the common path spills (e4m3 at T=16384 d=7168 133 us
+        // against 131).
+        const int sh = __double2hiint(ss) & 0x7FFFFFFF;   // compared as its high word; a NaN may have either sign
+        if (sh >= kDoubleInf || (sh < kDoubleLow && a.eps < 0x1p-110f)) {
+            const bool low = sh < kDoubleLow;
+            const float c = low ? 0x1p64f : 0x1p-70f;
+            double s2 = 0.0;
+#pragma unroll
+            for (int i = 0; i < WPT; i++) {
+                const int v = i * gt + ti;
+                if (v < nw) {
+                    u[i] = load16((a.residual ? a.xsum : a.x) + base + 16 * v, a.al32);
+                    s2 += (double)squares8(u[i].lo, c) + (double)squares8(u[i].hi, c);
+                }
+            }
+            ss = group_sum(s2, s_sum[1] + group * warps, group, warps) * (low ? 0x1p-128 : 0x1p140);
+        }
+        // var = 4^e m with m in [1/4, 1), and 1 / sqrt(m) is r0 + r1, in (1, 2]: r0 from rsqrtf
+        // (within 2 units in the last place), r1 one Newton step from its residual 1 - m r0^2.
+        // 2^-e s w is then y or down to half of it: it leaves the range only where y does (s w
+        // itself may: the multiplication by 2^-e costs e4m3 and int8 2 of their 131 us).
+        // The two products are exact, and y is rounded to fp32 once before it is to bf16: a
+        // y whose last place differs from the definition's can flip a code.
         const double var = ss * a.inv_d + (double)a.eps;
-        const float vh = (float)var, vl = (float)(var - (double)vh);
+        const int vx = __double2hiint(var) & 0x7FFFFFFF;
+        const bool finite = vx < kDoubleInf;
+        const int e = finite ? (((vx >> 20) - 1023) >> 1) + 1 : 0;
+        const double m = __hiloint2double(vx - 2 * e * (1 << 20), __double2loint(var));
+        const float p = __uint_as_float(e < 127 ? (uint32_t)(127 - e) << 23 : 0x00400000u >> (e - 127));   // 2^-e, e <= 128
+        const float vh = (float)m, vl = (float)(m - (double)vh);
         const float r0 = rsqrtf(vh), h = vh * r0;
         const float res = fmaf(-h, r0, 1.f) - (fmaf(vh, r0, -h) + vl * r0) * r0;
-        const float r1 = vh < 3.0e38f ? 0.5f * r0 * res : 0.f;   // an infinite mean keeps r0 = 0
+        const float r1 = finite ? 0.5f * r0 * res : 0.f;   // an infinite mean keeps r0 = 0
 #pragma unroll
         for (int i = 0; i < WPT; i++) {
             const int v = i * gt + ti;
             if (v < nw) {
                 const v16 wv = load16(a.weight + 16 * v, a.al32);
-                u[i].lo = scale_bf16x8(u[i].lo, wv.lo, r0, r1);
-                u[i].hi = scale_bf16x8(u[i].hi, wv.hi, r0, r1);
+                u[i].lo = scale_bf16x8(u[i].lo, wv.lo, p, r0, r1);
+                u[i].hi = scale_bf16x8(u[i].hi, wv.hi, p, r0, r1);
                 if (OUT == NORM_BF16 || a.y) store16(a.y + base + 16 * v, u[i], a.al32);
             }
         }

@@ -267,10 +267,12 @@ MOE_API int moe_layer_forward_fp4(const moe_bf16 *x, const moe_bf16 *Wg, const f
  * layer:
  *   s = bf16(x + residual)                       (residual NULL: s = x)
  *   y = bf16( s / sqrt(mean(s^2) + eps) * weight )
- * x, residual, s (xsum), y [T,d]; weight [d]; eps > 0.  Sums are fp32.  xsum is
- * the stream to add the layer's output to; it is given exactly when residual
- * is, and may be x or residual itself; y may be x.  Other overlaps are not
- * allowed.  d is a multiple of 64 (128 for FP8), at most 32768. */
+ * x, residual, s (xsum), y [T,d]; weight [d]; eps > 0.  The mean and the root are
+ * carried beyond fp32, and no step before y leaves its range unless y does, whatever
+ * the size of s and weight.  A row with an infinite s has y = 0 in its finite places
+ * and NaN in the others; a row with a NaN is NaN.  xsum is the stream to add the
+ * layer's output to; it is given exactly when residual is, and may be x or residual
+ * itself; y may be x.  Other overlaps are not allowed.  d is a multiple of 64 (128 for FP8), at most 32768. */
 MOE_API int moe_rmsnorm(const moe_bf16 *x, const moe_bf16 *residual, const moe_bf16 *weight, int64_t T, int64_t d,
                         float eps, moe_bf16 *xsum, moe_bf16 *y, void *stream);
 
