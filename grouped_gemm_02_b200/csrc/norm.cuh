@@ -29,6 +29,7 @@
 namespace moe {
 
 constexpr int kNormMaxD = 32768;             // 1024 threads x 32 values
+constexpr float kMaxFloat = 3.402823466e+38f;
 constexpr int kDoubleInf = 0x7FF00000, kDoubleLow = (1023 - 50) << 20;   // high words of infinity and of 2^-50
 constexpr int NORM_BF16 = 0, NORM_FP8 = 1, NORM_INT8 = 2;
 
@@ -531,6 +532,42 @@ __host__ __device__ inline int64_t norm_grad_ctas(int64_t T, int d)
 
 constexpr int kNormGradSmemBytes = 200 * 1024;   // the most any shape takes (d = 16384: two stages of 512 x 4 vectors)
 
+// A row's sums in 64 bits, for one whose sums left fp32 (the same for its whole group).
+// `mine`: this thread's vectors of s, then of dy, blockDim.x apart.  Loops that are not unrolled
+// leave the common path its registers; with more than 512 threads, which have 64 each,
+// it is inlined (T=256 d=32768 30.4 us against 32.5 by a call), else called (T=4099
+// d=2048 15.6 us against 16.6 inlined).
+template <int VPT>
+__device__ __forceinline__ double2 norm_grad_sums64(const uint4* mine, const bf16* weight, int d, int warps)
+{
+    __shared__ double slot[2][32];
+    const int nt = (int)blockDim.x, nvec = d / 8, gt = warps * 32;
+    const int group = (int)threadIdx.x / gt, ti = (int)threadIdx.x - group * gt;
+    double ss = 0.0, dot = 0.0;
+#pragma unroll 1
+    for (int i = 0; i < VPT; i++) {
+        if (i * gt + ti >= nvec) continue;
+#pragma unroll 1
+        for (int j = 0; j < 4; j++) {
+            const float2 s = f2_get(f2_bf16(reinterpret_cast<const uint32_t*>(mine + i * nt)[j]));
+            const float2 g = f2_get(f2_bf16(reinterpret_cast<const uint32_t*>(mine + (VPT + i) * nt)[j]));
+            const float2 w = f2_get(f2_bf16(__ldg(reinterpret_cast<const uint32_t*>(weight) + 4 * (i * gt + ti) + j)));
+            ss += (double)s.x * s.x + (double)s.y * s.y;
+            dot += (double)g.x * w.x * s.x + (double)g.y * w.y * s.y;
+        }
+    }
+    // the scratch was last read before the barrier of this row's fp32 sums
+    ss = group_sum(ss, slot[0] + group * warps, group, warps);
+    dot = group_sum(dot, slot[1] + group * warps, group, warps);
+    return make_double2(ss, dot);
+}
+
+template <int VPT>
+__device__ __noinline__ double2 norm_grad_sums64_call(const uint4* mine, const bf16* weight, int d, int warps)
+{
+    return norm_grad_sums64<VPT>(mine, weight, d, warps);
+}
+
 template <int VPT, int MAXT>
 __global__ void __launch_bounds__(MAXT) rmsnorm_grad_kernel(const NormGradArgs a, int warps, int stages)
 {
@@ -608,8 +645,17 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_grad_kernel(const NormGradArgs a
             ss = warp_sum(lane < warps ? s_red[par][0][group * warps + lane] : 0.f);
             dot = warp_sum(lane < warps ? s_red[par][1][group * warps + lane] : 0.f);
         }
-        const float rstd = rsqrtf(ss / (float)a.d + a.eps);
-        const float m = dot * rstd / (float)a.d;      // mean(g * n)
+        float rstd = rsqrtf(ss / (float)a.d + a.eps);
+        float m = dot * rstd / (float)a.d;            // mean(g * n)
+        // a sum beyond fp32 (a value above 1.8e19, or a product of the three), or squares
+        // below it that count because eps is as small
+        if (!(ss <= kMaxFloat && fabsf(m) <= kMaxFloat) || (ss < 0x1p-80f && a.eps < 0x1p-110f)) {
+            const double2 q = MAXT > 512 ? norm_grad_sums64<VPT>(mine, a.weight, a.d, warps)
+                                         : norm_grad_sums64_call<VPT>(mine, a.weight, a.d, warps);
+            const double r = 1.0 / sqrt(q.x / (double)a.d + (double)a.eps);
+            rstd = (float)r;
+            m = (float)(q.y * r / (double)a.d);
+        }
         const f2 rstd2 = f2_of(rstd, rstd), mneg2 = f2_of(-m, -m);
 #pragma unroll
         for (int i = 0; i < VPT; i++) {
