@@ -31,6 +31,7 @@ from __future__ import annotations
 import dataclasses
 import math
 import zlib
+from concurrent.futures import ThreadPoolExecutor
 from typing import Dict, Optional
 
 import numpy as np
@@ -132,10 +133,15 @@ def make_inputs(s: LayerShape, seed: int = 0, device="cpu",
 
 
 def make_weights(s: LayerShape, seed: int = 0, device="cpu") -> Dict[str, torch.Tensor]:
-    w: Dict[str, torch.Tensor] = {}
-    w["W1"] = _normal_bf16((s.E, s.f, s.d), 1.0 / math.sqrt(s.d), seed, "W1", device)
-    w["W3"] = _normal_bf16((s.E, s.f, s.d), 1.0 / math.sqrt(s.d), seed, "W3", device)
-    w["W2"] = _normal_bf16((s.E, s.d, s.f), 1.0 / math.sqrt(s.f), seed, "W2", device)
+    std_d, std_f = 1.0 / math.sqrt(s.d), 1.0 / math.sqrt(s.f)
+    spec = {"W1": ((s.E, s.f, s.d), std_d), "W3": ((s.E, s.f, s.d), std_d), "W2": ((s.E, s.d, s.f), std_f)}
+    draw = lambda n: _normal_bf16(spec[n][0], spec[n][1], seed, n, device)
+    if torch.device(device).type == "cpu":
+        # each tensor has a generator of its own and the host's draws one after another: three at a time
+        with ThreadPoolExecutor(len(spec)) as pool:
+            w = dict(zip(spec, pool.map(draw, spec)))
+    else:
+        w = {n: draw(n) for n in spec}
     w.update(make_shared_weights(s, seed, device))
     return w
 

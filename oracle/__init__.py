@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+from concurrent.futures import ThreadPoolExecutor
 from typing import Dict, Optional, Sequence
 
 import numpy as np
@@ -110,6 +111,20 @@ def default_threads() -> int:
     return int(lib().oracle_default_threads())
 
 
+def _in_parts(n: int, run, work: int, unit: int = 1) -> None:
+    """run(a, b) -> status for ranges that cover 0..n in whole units, on one thread a core.  Rows do not depend on
+    one another and each is computed as it would be alone, so the split changes no result; a job of little work
+    (counted in inner steps) stays whole."""
+    parts = min(default_threads(), n // unit, work >> 18)
+    if parts <= 1:
+        _check(run(0, n), run.__name__)
+        return
+    cut = [n // unit * i // parts * unit for i in range(parts)] + [n]
+    with ThreadPoolExecutor(parts) as pool:         # ctypes lets go of the interpreter lock for a call
+        for rc in pool.map(run, cut[:-1], cut[1:]):
+            _check(rc, run.__name__)
+
+
 def router_logits(x: np.ndarray, Wg: np.ndarray, bias: Optional[np.ndarray]) -> np.ndarray:
     """fp64 logits L[t,e] = sum_c x[t,c] Wg[e,c] + b[e]."""
     x, Wg = _u16(x), _u16(Wg)
@@ -117,8 +132,12 @@ def router_logits(x: np.ndarray, Wg: np.ndarray, bias: Optional[np.ndarray]) -> 
     E = Wg.shape[0]
     b = None if bias is None else np.ascontiguousarray(bias, dtype=np.float32)
     L = np.empty((T, E), dtype=np.float64)
-    _check(lib().oracle_router_logits(_ptr(x, C.c_uint16), _ptr(Wg, C.c_uint16), _ptr(b, C.c_float),
-                                      T, d, E, _ptr(L, C.c_double)), "router_logits")
+    fn = lib().oracle_router_logits
+
+    def router_logits_rows(a, b_):
+        return fn(_ptr(x[a:b_], C.c_uint16), _ptr(Wg, C.c_uint16), _ptr(b, C.c_float), b_ - a, d, E,
+                  _ptr(L[a:b_], C.c_double))
+    _in_parts(T, router_logits_rows, T * E * d)
     return L
 
 
@@ -228,8 +247,11 @@ def quantize_rows_fp8(x: np.ndarray):
     R, Cc = x.shape
     q = np.empty((R, Cc), dtype=np.uint8)
     sc = np.empty((R, Cc // 128), dtype=np.float64)
-    _check(lib().oracle_quantize_rows_fp8(_ptr(x, C.c_uint16), R, Cc, _ptr(q, C.c_uint8), _ptr(sc, C.c_double)),
-           "quantize_rows_fp8")
+    fn = lib().oracle_quantize_rows_fp8
+
+    def quantize_rows_fp8(a, b):
+        return fn(_ptr(x[a:b], C.c_uint16), b - a, Cc, _ptr(q[a:b], C.c_uint8), _ptr(sc[a:b], C.c_double))
+    _in_parts(R, quantize_rows_fp8, R * Cc)
     return q, sc
 
 
@@ -239,8 +261,12 @@ def quantize_blocks_fp8(W: np.ndarray):
     R, Cc = W.shape
     q = np.empty((R, Cc), dtype=np.uint8)
     sc = np.empty((R // 128, Cc // 128), dtype=np.float64)
-    _check(lib().oracle_quantize_blocks_fp8(_ptr(W, C.c_uint16), R, Cc, _ptr(q, C.c_uint8), _ptr(sc, C.c_double)),
-           "quantize_blocks_fp8")
+    fn = lib().oracle_quantize_blocks_fp8
+
+    def quantize_blocks_fp8(a, b):
+        return fn(_ptr(W[a:b], C.c_uint16), b - a, Cc, _ptr(q[a:b], C.c_uint8),
+                  _ptr(sc[a // 128:b // 128], C.c_double))
+    _in_parts(R, quantize_blocks_fp8, R * Cc, unit=128)
     return q, sc
 
 
@@ -309,9 +335,14 @@ def expert_h_fp8(xq, sx, W1q, s1, W3q, s3):
     f, d = W1q.shape
     hq = np.empty(f, dtype=np.uint8)
     sh = np.empty(f // 128, dtype=np.float64)
-    _check(lib().oracle_expert_h_fp8(_ptr(W1q, C.c_uint8), _ptr(s1, C.c_double), _ptr(W3q, C.c_uint8),
-                                     _ptr(s3, C.c_double), _ptr(xq, C.c_uint8), _ptr(sx, C.c_double), d, f,
-                                     _ptr(hq, C.c_uint8), _ptr(sh, C.c_double)), "expert_h_fp8")
+    fn = lib().oracle_expert_h_fp8
+
+    def expert_h_fp8_rows(a, b):     # h is requantised in blocks of 128 rows of W1 and W3
+        ab, bb = a // 128, b // 128
+        return fn(_ptr(W1q[a:b], C.c_uint8), _ptr(s1[ab:bb], C.c_double), _ptr(W3q[a:b], C.c_uint8),
+                  _ptr(s3[ab:bb], C.c_double), _ptr(xq, C.c_uint8), _ptr(sx, C.c_double), d, b - a,
+                  _ptr(hq[a:b], C.c_uint8), _ptr(sh[ab:bb], C.c_double))
+    _in_parts(f, expert_h_fp8_rows, f * d, unit=128)
     return hq, sh
 
 
@@ -337,8 +368,11 @@ def quantize_rows_fp4(W: np.ndarray):
     R, Cc = W.shape
     q = np.empty((R, Cc), dtype=np.uint8)
     sc = np.empty((R, Cc // 32), dtype=np.float64)
-    _check(lib().oracle_quantize_rows_fp4(_ptr(W, C.c_uint16), R, Cc, _ptr(q, C.c_uint8), _ptr(sc, C.c_double)),
-           "quantize_rows_fp4")
+    fn = lib().oracle_quantize_rows_fp4
+
+    def quantize_rows_fp4(a, b):
+        return fn(_ptr(W[a:b], C.c_uint16), b - a, Cc, _ptr(q[a:b], C.c_uint8), _ptr(sc[a:b], C.c_double))
+    _in_parts(R, quantize_rows_fp4, R * Cc)
     return q, sc
 
 

@@ -367,16 +367,15 @@ uint8_t oracle_e4m3_encode_fast(double v)
     return sign | (uint8_t)((field << 3) | (int)m);
 }
 
+/* The 256 values, tabulated when the library is loaded: the FFN loops read one per operand. */
 static double g_e4m3[256];
-static pthread_once_t g_e4m3_once = PTHREAD_ONCE_INIT;
-static void e4m3_table_init(void)
+__attribute__((constructor)) static void e4m3_table_init(void)
 {
     for (int c = 0; c < 256; c++)
         g_e4m3[c] = oracle_e4m3_decode((uint8_t)c);
 }
 static double e4m3_value(uint8_t c)
 {
-    pthread_once(&g_e4m3_once, e4m3_table_init);
     return g_e4m3[c];
 }
 
@@ -637,11 +636,23 @@ int oracle_moe_ffn_fp8(const uint8_t *xq, const double *sx,
  * blocks, as in the FP8 path.
  * ------------------------------------------------------------------------ */
 
-double oracle_e2m1_decode(uint8_t code)
+static double e2m1_define(uint8_t code)
 {
     int sign = (code >> 3) & 1, e = (code >> 1) & 3, m = code & 1;
     double v = e == 0 ? 0.5 * m : ldexp(1.0 + 0.5 * m, e - 1);
     return sign ? -v : v;
+}
+
+/* The 16 values, tabulated when the library is loaded (bits past the low four count for nothing). */
+static double g_e2m1[16];
+__attribute__((constructor)) static void e2m1_table_init(void)
+{
+    for (int c = 0; c < 16; c++)
+        g_e2m1[c] = e2m1_define((uint8_t)c);
+}
+double oracle_e2m1_decode(uint8_t code)
+{
+    return g_e2m1[code & 15];
 }
 
 /* Nearest e2m1 code to v (ties to the code with an even mantissa), saturating to 6. */
