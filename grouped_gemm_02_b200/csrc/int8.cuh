@@ -29,7 +29,7 @@
 // weights may be the output of the kernel before (a quantiser).
 //
 // Bound: at prefill the tensor cores, under the power cap (T=4096 K=7168 N=4096 on
-// one B200: 77 us, 3.1 PTOP/s, tensor pipe 71% active); at K = 2048 and below the
+// one B200: 77 us, 3.1 PTOP/s, tensor pipe 86% of the active cycles); at K = 2048 and below the
 // epilogue's stores beside the loads (T=8192 N=7168 98 us, 2.5 PTOP/s; without its
 // stores 74); at decode HBM (256 rows over 53 experts, K=N=2048: 41 us, 5.4 TB/s).
 #pragma once

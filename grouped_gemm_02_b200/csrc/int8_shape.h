@@ -32,11 +32,12 @@ struct Int8Shape {
 // draws from L2 (92 bytes/ns) and its MMAs (1.4 ns a column); a tile costs 215 ns
 // more, and the last one's epilogue 7 ns a column.  Pairs start 2.8 us later.
 // Joining a shared tile costs 2.2 us, 30 ns a CTA and 19 ns a column.  The constants
-// were fitted to 2,340 timings on a B200 (T 1..4096, K 512..16384, N 512..7168, every
-// form and row count): the cut with the smallest cost is within 1% of the fastest
-// one measured in the geometric mean, within 9% for every size.  A fixed 256 rows a
-// tile is up to 2.8 times slower where few tiles leave SMs idle: T=256 K=16384
-// N=2048 48 us against 17.
+// were fitted when every box of rows was 16 or 64 high.  Checked on the present
+// kernel, 2,967 timings on a B200 of every form, row count and cluster size at 121
+// sizes (T 1..4096, K 512..16384, N 512..7168): the cut with the smallest cost is
+// within 0.8% of the fastest one measured in the geometric mean, within 8.5% for every
+// size.  Always 256 rows a tile on single CTAs (fewer where T is smaller) is up to 2.7
+// times slower where few tiles leave SMs idle: T=256 K=16384 N=2048 49 us against 18.
 inline double i8_cost(int64_t T, int64_t K, int64_t N, int sms, int form, int chunk, int split)
 {
     const int64_t units = (T + chunk - 1) / chunk;

@@ -9,13 +9,13 @@
 //          moe_quantize_int8_rows (one scale a row), bit for bit
 //
 // Roundings: s once (the stream is kept in bf16 and the norm is of what is
-// kept), y once, and the codes are taken from the rounded y, so that a router
-// that reads y and experts that read q see the same row.
+// kept), y once, and the codes are taken from the rounded y, so that what reads
+// y and what reads q see the same row.
 //
 // Bound: HBM.  Every input is read once and every output written once: a row
 // stays in the registers of one group of warps between the reduction and the
-// normalisation.  T=16384 d=7168 with a residual on one B200: bf16 137 us (6.9
-// TB/s), e4m3 131 us (6.3 TB/s), int8 133 us (6.2 TB/s); the gradient at T=4099
+// normalisation.  T=16384 d=7168 with a residual on one B200: bf16 137 us (6.8
+// TB/s), e4m3 132 us (6.2 TB/s), int8 134 us (6.1 TB/s); the gradient at T=4099
 // d=7168 42 us (5.6 TB/s).  Next to the bytes it is the instructions that count (the
 // e4m3 form issues in two thirds of its slots), so the arithmetic runs on pairs of
 // fp32 values.
@@ -415,7 +415,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a, int war
         // var = 4^e m with m in [1/4, 1), and 1 / sqrt(m) is r0 + r1, in (1, 2]: r0 from rsqrtf
         // (within 2 units in the last place), r1 one Newton step from its residual 1 - m r0^2.
         // 2^-e s w is then y or down to half of it: it leaves the range only where y does (s w
-        // itself may: the multiplication by 2^-e costs e4m3 and int8 2 of their 131 us).
+        // itself may: the multiplication by 2^-e costs e4m3 and int8 2 of their 132
+        // and 134 us).
         // The two products are exact, and y is rounded to fp32 once before it is to bf16: a
         // y whose last place differs from the definition's can flip a code.
         const double var = ss * a.inv_d + (double)a.eps;

@@ -231,12 +231,13 @@ __global__ void __launch_bounds__(kSortChunk) sort_small_kernel(const int32_t* _
 }
 
 // ---------------------------------------------------------------- back, and the gradient of sort
-// out[t] = sum_j w[t, j] rows[pos] + add[t]; w null: weights 1.  k <= KM, and a
-// thread takes V = 8 / KM vectors of a token's row, so that eight loads of 16 bytes
-// are in flight together whatever k is (with one vector a thread k = 1 reached 30%
-// of the bytes that k = 8 did: T=4093 d=7168 60 us against 17).  BRIEF: short rows, a
-// warp a token and four tokens a CTA; otherwise a CTA has one token, whose positions
-// and gates are then the same registers for every thread.
+// out[t] = sum_j w[t, j] rows[pos] + add[t]; w null: weights 1.  k <= KM (k rounded up
+// to 1, 2, 4 or 8), and a thread takes V = 8 / KM vectors of a token's row, so that
+// 5 to 8 loads of 16 bytes are in flight together (with one vector a thread k = 1
+// reached 30% of the bytes that k = 8 did: T=4093 d=7168 60 us against 17).  BRIEF:
+// short rows, a warp a token and four tokens a CTA; otherwise a CTA has one token, whose
+// positions and gates are then the same registers for every thread (a wide row is cut
+// over several CTAs, and each reads them).
 // add and out may be the same buffer (no __restrict__, no read-only loads): a vector
 // is read and then written by the same thread.  Reading a thread's vectors of add
 // ahead takes registers from calls without it (T=4093 d=7168 k=1 18.6 us against 16.6;

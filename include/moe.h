@@ -294,8 +294,8 @@ MOE_API int moe_rmsnorm_backward_workspace_size(int64_t T, int64_t d, size_t *by
  * n = s rstd and g = dy * weight:
  *   dx      = bf16( (g - n mean(g n)) rstd + dxsum )   [T,d]
  *   dweight = sum over rows of dy * n                  [d], fp32
- * in fp32; a row whose sums leave its range is summed in 64 bits, so only dy * weight
- * itself has to be within it.  A row of xsum with a NaN or an infinity has dx = NaN;
+ * in fp32; a row whose sums leave its range is summed in 64 bits, so that only g (and
+ * sqrt(d) times its largest magnitude in the row) has to be within it.  A row of xsum with a NaN or an infinity has dx = NaN;
  * in dweight a NaN reaches every column and an infinity its own.
  * dxsum [T,d] is the gradient that reaches the stream itself (NULL: none); dx is
  * the gradient of x and of residual alike, and may be dy or dxsum itself.  The
